@@ -14,7 +14,7 @@ import os
 
 from ._abi import (MOE_F32, MOE_BF16, MOE_OK, GATE_TOPK_SOFTMAX, GATE_SOFTMAX_TOPK,  # noqa: F401
                    GATE_SOFTMAX_TOPK_RENORM, GATE_SIGMOID_BIAS_RENORM, MoELayerDesc, MoEDebugOut,
-                   EXPORTED_SYMBOLS, LAYER_SYNC_BYTES, STATIC_SCRATCH_BYTES, lib_path,
+                   EXPORTED_SYMBOLS, OPS_SYMBOLS, LAYER_SYNC_BYTES, STATIC_SCRATCH_BYTES, lib_path,
                    load_library)
 
 __all__ = [
@@ -28,6 +28,8 @@ __all__ = [
     "moe_layer_workspace_size", "moe_layer_status", "moe_source_sha256", "MOE_ERR_WAIT",
     "layer_workspace", "layer_desc", "dtype_code", "LAYER_SYNC_BYTES",
     "MoELayerDesc", "MoEDebugOut",
+    "moe_rmsnorm", "moe_rmsnorm_backward", "moe_rmsnorm_backward_workspace_size",
+    "moe_combine_backward", "mx_pitch",
 ]
 
 _LIB = None
@@ -268,3 +270,7 @@ def debug_out(logits=None, topk_ids=None, topk_w=None, counts=None, offsets=None
     for i, ev in enumerate(stage_events or ()):
         o.stage_events[i] = ev
     return o
+
+
+from .ops import (moe_rmsnorm, moe_rmsnorm_backward,  # noqa: E402
+                  moe_rmsnorm_backward_workspace_size, moe_combine_backward, mx_pitch)

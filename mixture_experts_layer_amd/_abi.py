@@ -1,4 +1,4 @@
-"""ctypes declarations of the C ABI in include/moe.h."""
+"""ctypes declarations of the C ABI in include/moe.h and include/moe_ops.h."""
 from __future__ import annotations
 
 import ctypes
@@ -15,6 +15,7 @@ GATE_SIGMOID_BIAS_RENORM = 3
 _PKG = os.path.dirname(os.path.abspath(__file__))
 
 c_int, c_size_t, c_void_p, c_char_p = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_char_p
+c_float = ctypes.c_float
 
 
 class MoELayerDesc(ctypes.Structure):
@@ -78,11 +79,23 @@ _SIGS = {
     "moe_layer_static": (c_int, [ctypes.POINTER(MoELayerDesc), c_int, c_void_p, c_void_p,
                                  ctypes.POINTER(MoEDebugOut), c_void_p]),
 }
+# include/moe_ops.h
+_OPS_SIGS = {
+    "moe_rmsnorm": (c_int, [c_void_p, c_void_p, c_void_p, c_float, c_int, c_int, c_int, c_void_p,
+                            c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "moe_rmsnorm_backward_workspace_size": (c_size_t, [c_int, c_int, c_int]),
+    "moe_rmsnorm_backward": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int,
+                                     c_int, c_int, c_void_p, c_void_p, c_void_p, c_size_t,
+                                     c_void_p]),
+    "moe_combine_backward": (c_int, [c_void_p, c_int, c_void_p, c_int, c_void_p, c_void_p, c_int,
+                                     c_int, c_int, c_void_p, c_void_p, c_void_p]),
+}
 # bytes of the device array moe_layer_static uses as its workspace
 STATIC_SCRATCH_BYTES = 64 << 20
 # bytes at the start of a layer workspace that the decode path keeps between calls
 LAYER_SYNC_BYTES = 4096 + 1024 * 128
-EXPORTED_SYMBOLS = tuple(_SIGS)
+EXPORTED_SYMBOLS = tuple(_SIGS)          # of include/moe.h
+OPS_SYMBOLS = tuple(_OPS_SIGS)           # of include/moe_ops.h
 
 
 def lib_path():
@@ -104,7 +117,7 @@ def load_library():
     # kernels.
     import torch  # noqa: F401
     lib = ctypes.CDLL(path)
-    for name, (res, args) in _SIGS.items():
+    for name, (res, args) in {**_SIGS, **_OPS_SIGS}.items():
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args

@@ -15,8 +15,11 @@ from __future__ import annotations
 import glob
 import hashlib
 import os
+import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -24,7 +27,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libmoe_mi355x.so")
 SOURCES = ["abi.hip", "route.hip", "permute.hip", "ffn.hip", "combine.hip", "decode.hip",
-           "dispatch.hip", "reshard.hip"]
+           "dispatch.hip", "reshard.hip", "ops_abi.hip", "norm.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [
@@ -38,7 +41,7 @@ HIPCC_FLAGS = [
 def source_files():
     """Every file the library is compiled from, in a fixed order."""
     files = sorted(glob.glob(os.path.join(CSRC, "*.hip")) + glob.glob(os.path.join(CSRC, "*.h")))
-    return files + [os.path.join(ROOT, "include", "moe.h")]
+    return files + [os.path.join(ROOT, "include", h) for h in ("moe.h", "moe_ops.h")]
 
 
 def source_sha256():
@@ -60,17 +63,32 @@ def hipcc():
     raise RuntimeError("hipcc not found")
 
 
-def build(verbose=False):
-    os.makedirs(LIBDIR, exist_ok=True)
-    tmp = LIB + ".tmp"
-    stamp = f'-DMOE_SOURCE_SHA256="{source_sha256()}"'
-    cmd = [hipcc()] + HIPCC_FLAGS + [stamp] + [os.path.join(CSRC, s) for s in SOURCES] + ["-o", tmp]
+def _run(cmd, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError(f"hipcc failed with status {r.returncode}")
+
+
+def build(verbose=False):
+    """Compile every source, several at a time, and link them."""
+    os.makedirs(LIBDIR, exist_ok=True)
+    stamp = f'-DMOE_SOURCE_SHA256="{source_sha256()}"'
+    flags = [f for f in HIPCC_FLAGS if f != "-shared"]
+    objdir = tempfile.mkdtemp(prefix="moe_build_")
+    try:
+        objs = [os.path.join(objdir, s + ".o") for s in SOURCES]
+        cmds = [[hipcc()] + flags + [stamp, "-c", os.path.join(CSRC, s), "-o", o]
+                for s, o in zip(SOURCES, objs)]
+        with ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+            for _ in pool.map(lambda c: _run(c, verbose), cmds):
+                pass
+        tmp = LIB + ".tmp"
+        _run([hipcc(), "-shared", "-fPIC", f"--offload-arch={ARCH}"] + objs + ["-o", tmp], verbose)
+    finally:
+        shutil.rmtree(objdir)
     os.replace(tmp, LIB)
     return LIB
 

@@ -9,48 +9,18 @@
 #include <mutex>
 
 #include "moe.h"
+#include "moe_host.h"
 #include "moe_kernels.h"
 
 using namespace moe;
 
 namespace {
 
-constexpr size_t kAlign = 256;
-
-inline size_t align_up(size_t v) { return (v + kAlign - 1) & ~(kAlign - 1); }
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-inline int elt_bytes(int dt) { return dt == MOE_F32 ? 4 : 2; }
-inline bool valid_dt(int dt) { return dt == MOE_F32 || dt == MOE_BF16; }
-inline int cdiv(int a, int b) { return a / b + (a % b != 0); }   // a >= 0, b > 0, no overflow
-
-// Bump allocator over the caller's workspace (or a size count when base == 0).
-struct Carver {
-  char* base;
-  size_t used = 0;
-  explicit Carver(void* b) : base(static_cast<char*>(b)) {}
-  template <typename T>
-  T* take(size_t bytes) {
-    T* p = base ? reinterpret_cast<T*>(base + used) : nullptr;
-    used += align_up(bytes);
-    return p;
-  }
-};
-
-// Token-pair and logit counts are int on the device: T * E (logits; k <= E,
-// so this bounds the T * k pairs as well) must fit an int.
-bool fits_int(long long a, long long b) { return a * b <= INT_MAX; }
-
 int check_route_shape(int T, int E, int k, int mode) {
   if (T < 0 || E < 1 || k < 1 || k > E) return MOE_ERR_INVALID_ARG;
   if (mode < 0 || mode > 3) return MOE_ERR_INVALID_ARG;
   if (E > 1024 || k > KMAX) return MOE_ERR_UNSUPPORTED;
   if (!fits_int(T, E)) return MOE_ERR_UNSUPPORTED;
-  return MOE_OK;
-}
-
-int check_hidden(int H) {
-  if (H <= 0) return MOE_ERR_INVALID_ARG;
-  if (H % 32) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -141,14 +111,6 @@ size_t layer_layout(const moe_layer_desc* d, int T, void* base, LayerWs* w, int 
   if (w) *w = l;
   return c.used;
 }
-
-#define MOE_TRY(expr)                      \
-  do {                                     \
-    hipError_t _e = (expr);                \
-    if (_e != hipSuccess) return MOE_ERR_HIP; \
-  } while (0)
-
-inline int hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
 bool decode_shape_ok(const moe_layer_desc* d, int T) {
   return decode_supported(d->dt, T, d->E, d->e_end - d->e_begin, d->k, d->H, d->I_loc,

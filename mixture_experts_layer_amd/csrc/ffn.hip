@@ -556,9 +556,6 @@ __global__ __launch_bounds__(DCOLS_WAVES * 64) void ffn_direct_cols_kernel(Direc
 // consecutive numbers are mapped to one XCD (workgroups are dealt to the 8
 // XCDs round-robin) so that they share that XCD's L2.
 // ---------------------------------------------------------------------------
-typedef __attribute__((address_space(3))) void lds_void_t;
-typedef __attribute__((address_space(1))) void gbl_void_t;
-
 struct TileArgs {
   const bf16_t* X;
   const int32_t* src_token;
@@ -611,35 +608,8 @@ struct TileCfg {
 };
 
 
-// 16 bytes per lane from base + voff + soff into LDS at lds + 16 * lane, as a
-// raw-buffer load of a buffer of nbytes: the address is a scalar base, one
-// 32-bit lane offset and a scalar step, so a load costs no vector
-// instructions; bytes past nbytes read as zero.
-template <int AUX = 0>
-__device__ __forceinline__ void buffer_load_lds16(const void* base, uint32_t nbytes, void* lds,
-                                                  uint32_t voff, uint32_t soff) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  const __amdgpu_buffer_rsrc_t r =
-      __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, nbytes, 0x00020000);
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)lds, 16, voff, soff, 0, AUX);
-#endif
-}
-
 template <class C>
 __device__ __forceinline__ int tile_swz(int r) { return (r / C::RP256) % C::CPR; }
-
-// Wait until at most N vector-memory loads of this wave are outstanding and
-// all its LDS reads have returned, then meet the other waves.
-template <int N>
-__device__ __forceinline__ void wait_stage_barrier() {
-  static_assert(N < 64, "vmcnt range");
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"(N) : "memory");
-  // The same lgkmcnt(0) where the compiler can see it (a no-op at run time):
-  // its wait insertion does not read the asm, and believing an older scalar
-  // load still pending, it had made the stage's first MFMAs wait for every
-  // LDS read issued ahead of them instead of only their own.
-  __builtin_amdgcn_s_waitcnt(0xC07F);   // vmcnt(63) expcnt(7) lgkmcnt(0)
-}
 
 // A bf16 output tile leaves through LDS: the block's finished tile is staged
 // row by row (rows padded by 16 bytes so the column-wise writes spread over

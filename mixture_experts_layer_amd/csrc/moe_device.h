@@ -245,4 +245,34 @@ __device__ inline void wave_routing_metadata(const int* total, int E_loc, int ca
   }
 }
 
+typedef __attribute__((address_space(3))) void lds_void_t;
+typedef __attribute__((address_space(1))) void gbl_void_t;
+
+// 16 bytes per lane from base + voff + soff into LDS at lds + 16 * lane, as a
+// raw-buffer load of a buffer of nbytes: the address is a scalar base, one
+// 32-bit lane offset and a scalar step, so a load costs no vector
+// instructions; bytes past nbytes read as zero.
+template <int AUX = 0>
+__device__ __forceinline__ void buffer_load_lds16(const void* base, uint32_t nbytes, void* lds,
+                                                  uint32_t voff, uint32_t soff) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const __amdgpu_buffer_rsrc_t r =
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, nbytes, 0x00020000);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)lds, 16, voff, soff, 0, AUX);
+#endif
+}
+
+// Wait until at most N vector-memory loads of this wave are outstanding and
+// all its LDS reads have returned, then meet the other waves.
+template <int N>
+__device__ __forceinline__ void wait_stage_barrier() {
+  static_assert(N < 64, "vmcnt range");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"(N) : "memory");
+  // The same lgkmcnt(0) where the compiler can see it (a no-op at run time):
+  // its wait insertion does not read the asm, and believing an older scalar
+  // load still pending, it had made the stage's first MFMAs wait for every
+  // LDS read issued ahead of them instead of only their own.
+  __builtin_amdgcn_s_waitcnt(0xC07F);   // vmcnt(63) expcnt(7) lgkmcnt(0)
+}
+
 }  // namespace moe

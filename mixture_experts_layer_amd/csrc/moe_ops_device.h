@@ -1,0 +1,136 @@
+// Device helpers of the operators around the layer (norm, MXFP8 experts,
+// backward passes): rows in 8-element chunks, bfloat16 rounding by the
+// hardware conversion, MXFP8 blocks, and the lookup of an expert's row tile.
+#pragma once
+#include "moe_device.h"
+
+namespace moe {
+
+typedef __bf16 bf16x2_v __attribute__((ext_vector_type(2)));
+typedef float f32x2_v __attribute__((ext_vector_type(2)));
+
+// Two floats to packed bfloat16, to nearest even; NaN stays NaN (one
+// v_cvt_pk_bf16_f32).
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_v){lo, hi}, bf16x2_v));
+}
+
+// 8 consecutive elements of a bfloat16 or float32 row.
+template <bool BF16>
+struct Chunk {
+  uint4 raw[BF16 ? 1 : 2];
+  __device__ __forceinline__ void load(const void* row, int c) {
+    const uint4* p = reinterpret_cast<const uint4*>(row) + (BF16 ? c : 2 * c);
+    raw[0] = p[0];
+    if (!BF16) raw[BF16 ? 0 : 1] = p[1];
+  }
+  __device__ __forceinline__ void get(float* f) const {
+    if (BF16) {
+      unpack_bf16x8(raw[0], f);
+    } else {
+      const uint4 a = raw[0], b = raw[BF16 ? 0 : 1];
+      f[0] = __uint_as_float(a.x); f[1] = __uint_as_float(a.y);
+      f[2] = __uint_as_float(a.z); f[3] = __uint_as_float(a.w);
+      f[4] = __uint_as_float(b.x); f[5] = __uint_as_float(b.y);
+      f[6] = __uint_as_float(b.z); f[7] = __uint_as_float(b.w);
+    }
+  }
+  __device__ __forceinline__ void set(const float* f) {
+    if (BF16) {
+      raw[0] = make_uint4(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]), cvt_bf16x2(f[4], f[5]),
+                          cvt_bf16x2(f[6], f[7]));
+    } else {
+      raw[0] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                          __float_as_uint(f[3]));
+      raw[BF16 ? 0 : 1] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]),
+                                     __float_as_uint(f[6]), __float_as_uint(f[7]));
+    }
+  }
+  __device__ __forceinline__ void store(void* row, int c) const {
+    uint4* p = reinterpret_cast<uint4*>(row) + (BF16 ? c : 2 * c);
+    p[0] = raw[0];
+    if (!BF16) p[1] = raw[BF16 ? 0 : 1];
+  }
+};
+
+__device__ __forceinline__ size_t row_bytes(bool bf16, int H) { return (size_t)H * (bf16 ? 2 : 4); }
+
+// Sum over the 64 lanes of a wave in float64, the same bits in every lane: the
+// lane exchanges of wave_sum_f on both halves of the value.
+__device__ __forceinline__ double wave_sum_d(double v) {
+  auto dpp = [](double x, auto ctrl) {
+    const uint2 u = __builtin_bit_cast(uint2, x);
+    const uint2 r = make_uint2(
+        __builtin_amdgcn_update_dpp(0, (int)u.x, decltype(ctrl)::value, 0xF, 0xF, false),
+        __builtin_amdgcn_update_dpp(0, (int)u.y, decltype(ctrl)::value, 0xF, 0xF, false));
+    return __builtin_bit_cast(double, r);
+  };
+  v += dpp(v, std::integral_constant<int, 0xB1>{});    // quad_perm [1,0,3,2]
+  v += dpp(v, std::integral_constant<int, 0x4E>{});    // quad_perm [2,3,0,1]
+  v += dpp(v, std::integral_constant<int, 0x141>{});   // row_half_mirror
+  v += dpp(v, std::integral_constant<int, 0x140>{});   // row_mirror
+  uint2 u = __builtin_bit_cast(uint2, v);
+  auto lo = __builtin_amdgcn_permlane16_swap(u.x, u.x, false, false);
+  auto hi = __builtin_amdgcn_permlane16_swap(u.y, u.y, false, false);
+  v = __builtin_bit_cast(double, make_uint2(lo[0], hi[0])) +
+      __builtin_bit_cast(double, make_uint2(lo[1], hi[1]));
+  u = __builtin_bit_cast(uint2, v);
+  lo = __builtin_amdgcn_permlane32_swap(u.x, u.x, false, false);
+  hi = __builtin_amdgcn_permlane32_swap(u.y, u.y, false, false);
+  return __builtin_bit_cast(double, make_uint2(lo[0], hi[0])) +
+         __builtin_bit_cast(double, make_uint2(lo[1], hi[1]));
+}
+
+// Sum over a block of whole waves, the same bits in every thread: each wave's
+// sum, then the waves' sums in wave order.  `red`: one float per wave, not
+// read or written by anyone between two calls' barriers (callers alternate).
+__device__ __forceinline__ float wave_sum(float v) { return wave_sum_f(v); }
+__device__ __forceinline__ double wave_sum(double v) { return wave_sum_d(v); }
+template <typename F>
+__device__ __forceinline__ F block_sum(F v, F* red) {
+  v = wave_sum(v);
+  const int nw = blockDim.x >> 6;
+  if (nw == 1) return v;
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  lds_barrier();
+  F s = red[0];
+  for (int w = 1; w < nw; ++w) s += red[w];
+  return s;
+}
+
+// Largest of the four lanes of a quad (lanes 4q .. 4q + 3), in every lane.
+__device__ __forceinline__ float quad_max(float v) {
+  auto dpp = [](float x, auto ctrl) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+                                         0, __builtin_bit_cast(int, x), decltype(ctrl)::value, 0xF,
+                                         0xF, false));
+  };
+  v = fmaxf(v, dpp(v, std::integral_constant<int, 0xB1>{}));   // quad_perm [1,0,3,2]
+  return fmaxf(v, dpp(v, std::integral_constant<int, 0x4E>{}));   // quad_perm [2,3,0,1]
+}
+
+// ---------------------------------------------------------------------------
+// MXFP8 (OCP microscaling): 32 elements share the scale 2^(byte - 127); an
+// element is e4m3 (largest finite 448 = 1.75 * 2^8).  The byte is the least
+// one for which no element of the block exceeds 448 after scaling: with
+// max|v| = 1.m * 2^(E - 127) that is E - 8, one more if 1.m > 1.75, and at
+// least 0.  (The format's own suggestion, floor(log2 max|v|) - 8, saturates
+// every block whose largest element lies above 1.75 * 2^n; the larger scale
+// costs such a block one bit at the small end instead.)
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t mx_scale_byte(float amax) {
+  const uint32_t u = __float_as_uint(amax) & 0x7fffffffu;
+  const int b = (int)(u >> 23) - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return (uint32_t)max(b, 0);
+}
+// 2^(127 - byte), the factor an element is multiplied by (byte <= 248)
+__device__ __forceinline__ float mx_inv_scale(uint32_t byte) {
+  return __uint_as_float((254u - byte) << 23);
+}
+// four scaled values to e4m3, to nearest even
+__device__ __forceinline__ uint32_t mx_pack4(float a, float b, float c, float d) {
+  int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
+}
+
+}  // namespace moe

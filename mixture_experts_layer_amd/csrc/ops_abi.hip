@@ -1,0 +1,82 @@
+// C ABI entry points of the operators around the layer: argument checks,
+// workspace layout and kernel sequencing.  Declarations and the full contract
+// are in include/moe_ops.h.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <climits>
+#include <cmath>
+
+#include "moe_ops.h"
+#include "moe_host.h"
+#include "moe_kernels.h"
+#include "moe_ops_kernels.h"
+
+using namespace moe;
+
+namespace {
+
+template <typename... P>
+bool any_misaligned(const P*... p) {
+  return !(... && aligned16(p));   // a null pointer counts as aligned
+}
+
+int check_row_width(int H) {
+  const int st = check_hidden(H);
+  if (st) return st;
+  return H > OPS_MAX_H ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_rmsnorm(const void* x, const void* residual, const void* weight, float eps, int T, int H,
+                int dt, void* sum, void* y, void* y8, uint8_t* y8_scale, float* rstd,
+                void* stream) {
+  if (!valid_dt(dt) || T < 0 || !(eps >= 0.f) || std::isinf(eps)) return MOE_ERR_INVALID_ARG;
+  const int st = check_row_width(H);
+  if (st) return st;
+  if (!y8 != !y8_scale) return MOE_ERR_INVALID_ARG;
+  if (!sum && !y && !y8 && !rstd) return MOE_ERR_INVALID_ARG;
+  if (any_misaligned(x, residual, weight, sum, y, y8, y8_scale, rstd)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!x || !weight) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_rmsnorm(x, residual, weight, eps, T, H, dt, sum, y, y8, y8_scale, rstd,
+                                   static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_rmsnorm_backward_workspace_size(int T, int H, int dt) {
+  if (T < 0 || !valid_dt(dt) || check_row_width(H) != MOE_OK) return 0;
+  return align_up((size_t)(T > 0 ? rmsnorm_bwd_blocks(T) : 1) * H * 4);
+}
+
+int moe_rmsnorm_backward(const void* dy, const void* dsum, const void* s, const void* weight,
+                         const float* rstd, int T, int H, int dt, void* dx, float* dweight,
+                         void* ws, size_t ws_bytes, void* stream) {
+  if (!valid_dt(dt) || T < 0) return MOE_ERR_INVALID_ARG;
+  const int st = check_row_width(H);
+  if (st) return st;
+  if (!dweight || (T > 0 && (!dy || !s || !weight || !rstd || !dx))) return MOE_ERR_INVALID_ARG;
+  if (any_misaligned(dy, dsum, s, weight, rstd, dx, dweight, ws)) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!ws || ws_bytes < moe_rmsnorm_backward_workspace_size(T, H, dt)))
+    return MOE_ERR_WORKSPACE;
+  return hip_status(launch_rmsnorm_bwd(dy, dsum, s, weight, rstd, T, H, dt, dx, dweight,
+                                       static_cast<float*>(ws), static_cast<hipStream_t>(stream)));
+}
+
+int moe_combine_backward(const void* dy, int dt, const void* y_perm, int y_perm_dt,
+                         const int32_t* dst_row, const float* topk_w, int T, int k, int H,
+                         void* dy_perm, float* dtopk_w, void* stream) {
+  if (!valid_dt(dt) || !valid_dt(y_perm_dt) || T < 0 || k < 1) return MOE_ERR_INVALID_ARG;
+  const int st = check_row_width(H);
+  if (st) return st;
+  if (k > KMAX || !fits_int(T, k)) return MOE_ERR_UNSUPPORTED;
+  if (any_misaligned(dy, y_perm, dst_row, topk_w, dy_perm, dtopk_w)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!dy || !y_perm || !dst_row || !topk_w || !dy_perm || !dtopk_w) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_combine_bwd(dy, dt, y_perm, y_perm_dt, dst_row, topk_w, T, k, H,
+                                       dy_perm, dtopk_w, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

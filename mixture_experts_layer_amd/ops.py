@@ -1,0 +1,106 @@
+"""Python binding of the operators around the layer (include/moe_ops.h), with
+the names and argument orders of the C entry points.
+
+Arguments are contiguous torch tensors on one GPU (or None for NULL).  Unlike
+the raw C entry points, which see only addresses, a call here refuses a tensor
+whose type, layout, size or device is not what the entry point will read; it
+runs on that GPU's current stream unless `stream` names another of its
+streams.
+"""
+from __future__ import annotations
+
+from ._abi import MOE_BF16, MOE_F32
+
+def mx_pitch(K: int) -> int:
+    """Scale bytes of an MXFP8 row of K elements (MOE_MX_PITCH)."""
+    return (K + 127) // 128 * 4
+
+
+_TORCH = _LIB = _TYPES = None
+
+
+def _setup():
+    global _TORCH, _LIB, _TYPES
+    import torch
+
+    from . import get_lib
+    _TORCH = torch
+    _TYPES = {MOE_F32: (torch.float32,), MOE_BF16: (torch.bfloat16,), "f": (torch.float32,),
+              "i": (torch.int32,), "b": (torch.uint8,), "8": (torch.float8_e4m3fn, torch.uint8)}
+    _LIB = get_lib()
+
+
+def _call(fn, tensors, args, stream):
+    """Check `tensors` ((name, tensor or None, type, least elements) each) and
+    call the library's `fn` with `args`, in which a tensor stands for its
+    address, and the stream appended."""
+    if _LIB is None:
+        _setup()
+    dev = None
+    for name, t, kind, least in tensors:
+        if t is None:
+            continue
+        want = _TYPES.get(kind)
+        if want is not None and t.dtype not in want:
+            raise TypeError(f"{fn}: {name} is {t.dtype}, not {want[0]}")
+        if not t.is_contiguous():
+            raise ValueError(f"{fn}: {name} is not contiguous")
+        if t.numel() < least:
+            raise ValueError(f"{fn}: {name} holds {t.numel()} elements, fewer than {least}")
+        d = t.get_device()
+        if d != dev:
+            if d < 0 or dev is not None:
+                raise ValueError(f"{fn}: {name} is on {t.device}, not " +
+                                 ("a GPU" if dev is None else f"cuda:{dev}"))
+            dev = d
+    tensor = _TORCH.Tensor
+    argv = [a.data_ptr() if isinstance(a, tensor) else a for a in args]
+    here = _TORCH.cuda.current_device()
+    if dev is None or dev == here:
+        status = _launch(fn, argv, here, stream)
+    else:
+        with _TORCH.cuda.device(dev):
+            status = _launch(fn, argv, dev, stream)
+    if status != 0:
+        from . import MoEError
+        raise MoEError(fn, status)
+
+
+def _launch(fn, argv, dev, stream):
+    if stream is None:
+        # the handle of torch.cuda.current_stream(dev), without the stream object
+        stream = _TORCH._C._cuda_getCurrentRawStream(dev)
+    return getattr(_LIB, fn)(*argv, stream)
+
+
+def moe_rmsnorm(x, residual, weight, eps, T, H, dt, sum, y, y8, y8_scale, rstd, stream=None):
+    n = T * H
+    _call("moe_rmsnorm",
+          (("x", x, dt, n), ("residual", residual, dt, n), ("weight", weight, dt, H),
+           ("sum", sum, dt, n), ("y", y, dt, n), ("y8", y8, "8", n),
+           ("y8_scale", y8_scale, "b", T * mx_pitch(H)), ("rstd", rstd, "f", T)),
+          (x, residual, weight, eps, T, H, dt, sum, y, y8, y8_scale, rstd), stream)
+
+
+def moe_rmsnorm_backward_workspace_size(T, H, dt) -> int:
+    from . import lib
+    return lib.moe_rmsnorm_backward_workspace_size(T, H, dt)
+
+
+def moe_rmsnorm_backward(dy, dsum, s, weight, rstd, T, H, dt, dx, dweight, ws, ws_bytes,
+                         stream=None):
+    n = T * H
+    _call("moe_rmsnorm_backward",
+          (("dy", dy, dt, n), ("dsum", dsum, dt, n), ("s", s, dt, n), ("weight", weight, dt, H),
+           ("rstd", rstd, "f", T), ("dx", dx, dt, n), ("dweight", dweight, "f", H),
+           ("ws", ws, "b", ws_bytes)),
+          (dy, dsum, s, weight, rstd, T, H, dt, dx, dweight, ws, ws_bytes), stream)
+
+
+def moe_combine_backward(dy, dt, y_perm, y_perm_dt, dst_row, topk_w, T, k, H, dy_perm, dtopk_w,
+                         stream=None):
+    _call("moe_combine_backward",
+          (("dy", dy, dt, T * H), ("y_perm", y_perm, y_perm_dt, 0),
+           ("dst_row", dst_row, "i", T * k), ("topk_w", topk_w, "f", T * k),
+           ("dy_perm", dy_perm, y_perm_dt, 0), ("dtopk_w", dtopk_w, "f", T * k)),
+          (dy, dt, y_perm, y_perm_dt, dst_row, topk_w, T, k, H, dy_perm, dtopk_w), stream)

@@ -1,0 +1,122 @@
+"""The C ABI of the operators around the layer (include/moe_ops.h) on the
+host: declared, exported and bound alike, and bad arguments are rejected
+before anything reaches a GPU.  No call here gets to a kernel launch."""
+import ctypes
+import inspect
+import os
+import re
+import subprocess
+
+import pytest
+import torch
+
+import mixture_experts_layer_amd as M
+from conftest import ROOT
+
+HEADER = os.path.join(ROOT, "include", "moe_ops.h")
+INVALID, UNSUPPORTED, WORKSPACE = 1, 2, 3
+P, MIS = 1 << 20, (1 << 20) + 4        # stand-ins for device addresses
+
+
+def _header():
+    return re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+
+
+def test_declared_exported_and_bound_alike():
+    names = sorted(set(re.findall(r"\b(moe_[a-z0-9_]+)\s*\(", _header())))
+    assert names == sorted(M.OPS_SYMBOLS)
+    out = subprocess.run(["nm", "-D", "--defined-only", M.lib_path()], capture_output=True,
+                         text=True, check=True).stdout
+    assert set(names) <= set(re.findall(r"\sT\s(moe_\w+)", out))
+    for n in names:
+        assert n in M.__all__
+        args = re.search(n + r"\s*\(([^)]*)\)", _header()).group(1)
+        want = [a.split()[-1].lstrip("*") for a in args.split(",")]
+        got = list(inspect.signature(getattr(M, n)).parameters)
+        assert got == want, n
+        assert len(want) == len(getattr(M.get_lib(), n).argtypes)
+
+
+def test_mx_pitch():
+    macro = re.search(r"#define MOE_MX_PITCH\(K\) (.*)", open(HEADER).read()).group(1)
+    for K in (32, 96, 128, 160, 4096, 7168):
+        want = eval(macro.replace("(K)", str(K)).replace("/", "//"))
+        assert M.mx_pitch(K) == want >= K // 32 and want % 4 == 0
+
+
+def _st(fn, *args):
+    return getattr(M.lib, fn)(*args)
+
+
+NORM = dict(x=P, residual=P, weight=P, eps=1e-6, T=4, H=256, dt=1, sum=P, y=P, y8=P, y8_scale=P,
+            rstd=P, stream=0)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=-1), INVALID), (dict(dt=2), INVALID), (dict(dt=-1), INVALID),
+    (dict(eps=-1e-6), INVALID), (dict(eps=float("nan")), INVALID), (dict(eps=float("inf")), INVALID),
+    (dict(H=0), INVALID), (dict(H=-32), INVALID), (dict(H=100), UNSUPPORTED),
+    (dict(H=16416), UNSUPPORTED), (dict(x=None), INVALID), (dict(weight=None), INVALID),
+    (dict(y8=None), INVALID), (dict(y8_scale=None), INVALID),
+    (dict(sum=None, y=None, y8=None, y8_scale=None, rstd=None), INVALID),
+] + [({n: MIS}, INVALID) for n in ("x", "residual", "weight", "sum", "y", "y8", "y8_scale", "rstd")])
+def test_rmsnorm_rejects(kw, status):
+    a = dict(NORM, **kw)
+    assert _st("moe_rmsnorm", *a.values()) == status
+
+
+def test_rmsnorm_without_rows_is_a_no_op():
+    assert _st("moe_rmsnorm", *dict(NORM, T=0).values()) == 0
+    assert _st("moe_rmsnorm", *dict(NORM, T=0, x=None, weight=None).values()) == 0
+
+
+NORM_BWD = dict(dy=P, dsum=P, s=P, weight=P, rstd=P, T=4, H=256, dt=1, dx=P, dweight=P, ws=P,
+                ws_bytes=1 << 20, stream=0)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=-1), INVALID), (dict(dt=2), INVALID), (dict(H=0), INVALID), (dict(H=48), UNSUPPORTED),
+    (dict(H=16416), UNSUPPORTED), (dict(ws=None), WORKSPACE), (dict(ws_bytes=4 * 256 * 4 - 1), WORKSPACE),
+    (dict(T=0, dweight=None), INVALID),
+] + [({n: None}, INVALID) for n in ("dy", "s", "weight", "rstd", "dx", "dweight")]
+  + [({n: MIS}, INVALID) for n in ("dy", "dsum", "s", "weight", "rstd", "dx", "dweight", "ws")])
+def test_rmsnorm_backward_rejects(kw, status):
+    assert _st("moe_rmsnorm_backward", *dict(NORM_BWD, **kw).values()) == status
+
+
+def test_rmsnorm_backward_workspace():
+    q = M.moe_rmsnorm_backward_workspace_size
+    assert q(1, 256, 1) >= 256 * 4 and q(8192, 7168, 1) >= 7168 * 4
+    assert q(10 ** 9, 16384, 0) <= 1 << 30          # bounded however many rows
+    for bad in ((-1, 256, 1), (4, 100, 1), (4, 256, 2), (4, 16416, 1)):
+        assert q(*bad) == 0
+
+
+COMBINE = dict(dy=P, dt=1, y_perm=P, y_perm_dt=1, dst_row=P, topk_w=P, T=4, k=2, H=256, dy_perm=P,
+               dtopk_w=P, stream=0)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=-1), INVALID), (dict(k=0), INVALID), (dict(k=33), UNSUPPORTED), (dict(dt=5), INVALID),
+    (dict(y_perm_dt=-1), INVALID), (dict(H=0), INVALID), (dict(H=33), UNSUPPORTED),
+    (dict(H=16416), UNSUPPORTED), (dict(T=2 ** 30, k=2), UNSUPPORTED),
+] + [({n: None}, INVALID) for n in ("dy", "y_perm", "dst_row", "topk_w", "dy_perm", "dtopk_w")]
+  + [({n: MIS}, INVALID) for n in ("dy", "y_perm", "dst_row", "topk_w", "dy_perm", "dtopk_w")])
+def test_combine_backward_rejects(kw, status):
+    assert _st("moe_combine_backward", *dict(COMBINE, **kw).values()) == status
+
+
+def test_the_binding_refuses_what_an_address_would_not_show():
+    x = torch.zeros(4, 256, dtype=torch.bfloat16)
+    w = torch.zeros(256, dtype=torch.bfloat16)
+    args = lambda **kw: [dict(x=x, residual=None, weight=w, eps=1e-6, T=4, H=256, dt=1, sum=None,  # noqa: E731
+                              y=x, y8=None, y8_scale=None, rstd=None, **{})[n] if n not in kw else kw[n]
+                         for n in list(NORM)[:-1]]
+    with pytest.raises(ValueError, match="not a GPU"):
+        M.moe_rmsnorm(*args())
+    with pytest.raises(TypeError, match="x is torch.float32"):
+        M.moe_rmsnorm(*args(x=x.float()))
+    with pytest.raises(ValueError, match="not contiguous"):
+        M.moe_rmsnorm(*args(x=torch.zeros(4, 512, dtype=torch.bfloat16)[:, ::2]))
+    with pytest.raises(ValueError, match="fewer than"):
+        M.moe_rmsnorm(*args(x=x[:3]))
