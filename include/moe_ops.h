@@ -88,6 +88,46 @@ int moe_combine_backward(const void* dy, int dt, const void* y_perm, int y_perm_
                          const int32_t* dst_row, const float* topk_w, int T, int k, int H,
                          void* dy_perm, float* dtopk_w, void* stream);
 
+/*
+ * moe_grouped_ffn_train / moe_grouped_ffn_backward -- moe_grouped_ffn with
+ * what its backward pass needs, and that pass.
+ *   For expert i and every row r in [offsets[i], offsets[i+1]), with
+ *   a = x_perm[r], or x[src_token[r]] when x_perm == NULL:
+ *     forward   g = W_gate a, u = W_up a, h = SiLU(g) * u, y_perm[r] = W2 h,
+ *               gu[r] = [g | u]  (float32, [max_rows][2*I_loc])
+ *     backward  dh = W2^T dy_perm[r]
+ *               dg = dh * u * SiLU'(g), du = dh * SiLU(g),
+ *               SiLU'(g) = s (1 + g (1 - s)), s = 1 / (1 + exp(-g))
+ *               dx_perm[r] = W_gate^T dg + W_up^T du
+ *               dw13[i] = sum_r [dg | du] a^T,  dw2[i] = sum_r dy_perm[r] h^T
+ *   The backward pass reads g and u from gu and forms h anew.  h, dg and du
+ *   are rounded to dt before the products that read them, as h is in the
+ *   forward pass; g and u are kept unrounded, so a gradient passes one
+ *   rounding between its two products, as the output does.
+ *
+ *   dy_perm, dx_perm, y_perm: [max_rows][H]; dw13, dw2: shapes of w13, w2; all
+ *   dtype dt.  dx_perm may be NULL, and dw13 and dw2 together may be NULL (not
+ *   all three).  An expert without rows gets zero gradients; max_rows = 0
+ *   writes them for every expert.  The gradient of token t's row in the
+ *   gathered form is the sum of its copies' dx_perm rows: moe_combine with
+ *   weights 1.  Shape limits of moe_grouped_ffn; H and I_loc at most
+ *   65536 and H * I_loc at most 2^30.
+ *   An expert whose offsets leave [0, max_rows] or decrease is treated as one
+ *   without rows.  With src_token, every source must be a row of x (padding
+ *   sources of -1 are refused by no check and read row 0).
+ */
+size_t moe_grouped_ffn_train_workspace_size(int max_rows, int E_loc, int H, int I_loc, int dt);
+int moe_grouped_ffn_train(const void* x_perm, const void* x, const int32_t* src_token,
+                          const int32_t* offsets, int E_loc, int max_rows, int H, int I_loc,
+                          const void* w13, const void* w2, int dt, float* gu, void* y_perm,
+                          void* ws, size_t ws_bytes, void* stream);
+size_t moe_grouped_ffn_backward_workspace_size(int max_rows, int E_loc, int H, int I_loc, int dt);
+int moe_grouped_ffn_backward(const void* dy_perm, const void* x_perm, const void* x,
+                             const int32_t* src_token, const int32_t* offsets, int E_loc,
+                             int max_rows, int H, int I_loc, const void* w13, const void* w2,
+                             int dt, const float* gu, void* dx_perm, void* dw13, void* dw2,
+                             void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -29,7 +29,9 @@ __all__ = [
     "layer_workspace", "layer_desc", "dtype_code", "LAYER_SYNC_BYTES",
     "MoELayerDesc", "MoEDebugOut",
     "moe_rmsnorm", "moe_rmsnorm_backward", "moe_rmsnorm_backward_workspace_size",
-    "moe_combine_backward", "mx_pitch",
+    "moe_combine_backward", "mx_pitch", "moe_grouped_ffn_train",
+    "moe_grouped_ffn_train_workspace_size", "moe_grouped_ffn_backward",
+    "moe_grouped_ffn_backward_workspace_size",
 ]
 
 _LIB = None
@@ -273,4 +275,6 @@ def debug_out(logits=None, topk_ids=None, topk_w=None, counts=None, offsets=None
 
 
 from .ops import (moe_rmsnorm, moe_rmsnorm_backward,  # noqa: E402
-                  moe_rmsnorm_backward_workspace_size, moe_combine_backward, mx_pitch)
+                  moe_rmsnorm_backward_workspace_size, moe_combine_backward, mx_pitch,
+                  moe_grouped_ffn_train, moe_grouped_ffn_train_workspace_size,
+                  moe_grouped_ffn_backward, moe_grouped_ffn_backward_workspace_size)

@@ -89,6 +89,15 @@ _OPS_SIGS = {
                                      c_void_p]),
     "moe_combine_backward": (c_int, [c_void_p, c_int, c_void_p, c_int, c_void_p, c_void_p, c_int,
                                      c_int, c_int, c_void_p, c_void_p, c_void_p]),
+    "moe_grouped_ffn_train_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int]),
+    "moe_grouped_ffn_train": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int,
+                                      c_int, c_void_p, c_void_p, c_int, c_void_p, c_void_p,
+                                      c_void_p, c_size_t, c_void_p]),
+    "moe_grouped_ffn_backward_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int]),
+    "moe_grouped_ffn_backward": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int,
+                                         c_int, c_int, c_int, c_void_p, c_void_p, c_int, c_void_p,
+                                         c_void_p, c_void_p, c_void_p, c_void_p, c_size_t,
+                                         c_void_p]),
 }
 # bytes of the device array moe_layer_static uses as its workspace
 STATIC_SCRATCH_BYTES = 64 << 20

@@ -27,7 +27,8 @@ CSRC = os.path.join(PKG, "csrc")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libmoe_mi355x.so")
 SOURCES = ["abi.hip", "route.hip", "permute.hip", "ffn.hip", "combine.hip", "decode.hip",
-           "dispatch.hip", "reshard.hip", "ops_abi.hip", "norm.hip"]
+           "dispatch.hip", "reshard.hip", "ops_abi.hip", "norm.hip",
+           "ffn_train.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

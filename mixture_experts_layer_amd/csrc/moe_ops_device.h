@@ -15,6 +15,12 @@ __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_v){lo, hi}, bf16x2_v));
 }
 
+// 16 bytes, not to be read again by this launch
+__device__ __forceinline__ void st_nt16(void* p, const uint4& v) {
+  typedef unsigned int v4 __attribute__((ext_vector_type(4)));
+  __builtin_nontemporal_store((v4){v.x, v.y, v.z, v.w}, reinterpret_cast<v4*>(p));
+}
+
 // 8 consecutive elements of a bfloat16 or float32 row.
 template <bool BF16>
 struct Chunk {
@@ -132,5 +138,61 @@ __device__ __forceinline__ uint32_t mx_pack4(float a, float b, float c, float d)
   int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
 }
+
+// ---------------------------------------------------------------------------
+// Row tiles of the experts, looked up by each wave in the offsets themselves
+// (no map to build in a launch of its own): expert e has ceil(count / BM)
+// tiles, numbered expert after expert.  An expert whose range is not within
+// [0, max_rows], or runs backwards, has none.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ int expert_tiles(int o, int end, int BM, int max_rows) {
+  return o >= 0 && o < end && end <= max_rows ? (end - o + BM - 1) / BM : 0;
+}
+
+struct RowTile {
+  int e, off, end;   // expert and its row range
+  int first;         // number of its first tile
+};
+
+struct TileScan {
+  int per, incl, n;  // experts per lane, tiles up to and of this lane's experts
+  int total;
+
+  // every lane of a wave takes part; E <= 1024
+  __device__ __forceinline__ void init(const int32_t* offsets, int E, int BM, int max_rows) {
+    const int lane = threadIdx.x & 63;
+    per = (E + 63) >> 6;
+    n = 0;
+    for (int j = 0; j < per; ++j) {
+      const int e = lane * per + j;
+      if (e < E) n += expert_tiles(offsets[e], offsets[e + 1], BM, max_rows);
+    }
+    incl = wave_inclusive_scan(n);
+    total = __builtin_amdgcn_readlane(incl, 63);
+  }
+  // the expert of tile `tile` < total (the same in every lane)
+  __device__ __forceinline__ RowTile find(const int32_t* offsets, int E, int BM, int max_rows,
+                                          int tile) const {
+    const int lane = threadIdx.x & 63;
+    const int L = __builtin_ctzll(__ballot(incl > tile));
+    RowTile r{0, 0, 0, 0};
+    if (lane == L) {
+      int base = incl - n;
+      for (int j = 0; j < per; ++j) {
+        const int e = lane * per + j;
+        if (e >= E) break;
+        const int o = offsets[e], end = offsets[e + 1];
+        const int nt = expert_tiles(o, end, BM, max_rows);
+        if (tile < base + nt) {
+          r = RowTile{e, o, end, base};
+          break;
+        }
+        base += nt;
+      }
+    }
+    return RowTile{__builtin_amdgcn_readlane(r.e, L), __builtin_amdgcn_readlane(r.off, L),
+                   __builtin_amdgcn_readlane(r.end, L), __builtin_amdgcn_readlane(r.first, L)};
+  }
+};
 
 }  // namespace moe

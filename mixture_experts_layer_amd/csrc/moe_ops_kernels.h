@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace moe {
 
 constexpr int OPS_MAX_H = 16384;   // row elements the one-block-per-row kernels hold
@@ -24,5 +26,23 @@ hipError_t launch_rmsnorm_bwd(const void* dy, const void* dsum, const void* s, c
 hipError_t launch_combine_bwd(const void* dy, int dt, const void* y_perm, int y_perm_dt,
                               const int32_t* dst_row, const float* w, int T, int k, int H,
                               void* dy_perm, float* dw, hipStream_t st);
+
+// ffn_train.hip: the grouped SwiGLU experts in training.  H, I multiples of 32.
+struct TrainFfn {
+  const void* x;            // token rows, gathered by src_token, or permuted rows
+  const int32_t* src_token; // or null
+  const int32_t* offsets;   // [E + 1]
+  int E, max_rows, H, I, dt;
+  const void* w13;
+  const void* w2;
+  float* gu;                // [max_rows][2 I]: written by the forward pass, read by the backward
+  void* h;                  // [max_rows][I], workspace
+};
+constexpr int OPS_MAX_DIM = 65536;               // H and I of the expert blocks
+constexpr long long OPS_MAX_HI = 1ll << 30;      // H * I: an expert's weights within 4 GiB
+hipError_t launch_train_forward(const TrainFfn& f, void* y, hipStream_t st);
+// dgu: [max_rows][2 I], workspace; dx, or dw13 with dw2, may be null
+hipError_t launch_train_backward(const TrainFfn& f, const void* dy, void* dgu, void* dx, void* dw13,
+                                 void* dw2, hipStream_t st);
 
 }  // namespace moe

@@ -27,6 +27,17 @@ int check_row_width(int H) {
   return H > OPS_MAX_H ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
+// Shapes of an expert block beside the layer's own.
+int check_block(int max_rows, int E_loc, int H, int I_loc) {
+  if (E_loc < 1 || max_rows < 0 || I_loc <= 0) return MOE_ERR_INVALID_ARG;
+  const int st = check_hidden(H);
+  if (st) return st;
+  if (I_loc % 32 || E_loc > 1024 || H > OPS_MAX_DIM || I_loc > OPS_MAX_DIM ||
+      (long long)H * I_loc > OPS_MAX_HI)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -77,6 +88,67 @@ int moe_combine_backward(const void* dy, int dt, const void* y_perm, int y_perm_
   if (!dy || !y_perm || !dst_row || !topk_w || !dy_perm || !dtopk_w) return MOE_ERR_INVALID_ARG;
   return hip_status(launch_combine_bwd(dy, dt, y_perm, y_perm_dt, dst_row, topk_w, T, k, H,
                                        dy_perm, dtopk_w, static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_grouped_ffn_train_workspace_size(int max_rows, int E_loc, int H, int I_loc, int dt) {
+  if (!valid_dt(dt) || check_block(max_rows, E_loc, H, I_loc) != MOE_OK) return 0;
+  return align_up((size_t)(max_rows > 0 ? max_rows : 1) * I_loc * elt_bytes(dt));
+}
+
+int moe_grouped_ffn_train(const void* x_perm, const void* x, const int32_t* src_token,
+                          const int32_t* offsets, int E_loc, int max_rows, int H, int I_loc,
+                          const void* w13, const void* w2, int dt, float* gu, void* y_perm,
+                          void* ws, size_t ws_bytes, void* stream) {
+  if (!valid_dt(dt)) return MOE_ERR_INVALID_ARG;
+  const int st = check_block(max_rows, E_loc, H, I_loc);
+  if (st) return st;
+  if (any_misaligned(x_perm, x, src_token, offsets, w13, w2, gu, y_perm, ws))
+    return MOE_ERR_INVALID_ARG;
+  if (max_rows == 0) return MOE_OK;
+  if (!offsets || !w13 || !w2 || !gu || !y_perm || (!x_perm && (!x || !src_token)))
+    return MOE_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < moe_grouped_ffn_train_workspace_size(max_rows, E_loc, H, I_loc, dt))
+    return MOE_ERR_WORKSPACE;
+  const TrainFfn f{x_perm ? x_perm : x, x_perm ? nullptr : src_token, offsets, E_loc, max_rows, H,
+                   I_loc, dt, w13, w2, gu, ws};
+  return hip_status(launch_train_forward(f, y_perm, static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_grouped_ffn_backward_workspace_size(int max_rows, int E_loc, int H, int I_loc, int dt) {
+  if (!valid_dt(dt) || check_block(max_rows, E_loc, H, I_loc) != MOE_OK) return 0;
+  const size_t row = (size_t)I_loc * elt_bytes(dt), rows = max_rows > 0 ? max_rows : 1;
+  return align_up(rows * row) + align_up(rows * row * 2);
+}
+
+int moe_grouped_ffn_backward(const void* dy_perm, const void* x_perm, const void* x,
+                             const int32_t* src_token, const int32_t* offsets, int E_loc,
+                             int max_rows, int H, int I_loc, const void* w13, const void* w2,
+                             int dt, const float* gu, void* dx_perm, void* dw13, void* dw2,
+                             void* ws, size_t ws_bytes, void* stream) {
+  if (!valid_dt(dt)) return MOE_ERR_INVALID_ARG;
+  const int st = check_block(max_rows, E_loc, H, I_loc);
+  if (st) return st;
+  if (!dw13 != !dw2 || (!dx_perm && !dw2)) return MOE_ERR_INVALID_ARG;
+  if (any_misaligned(dy_perm, x_perm, x, src_token, offsets, w13, w2, gu, dx_perm, dw13, dw2, ws))
+    return MOE_ERR_INVALID_ARG;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (max_rows == 0) {
+    if (!dw2) return MOE_OK;
+    const size_t bytes = (size_t)E_loc * H * I_loc * elt_bytes(dt);
+    MOE_TRY(launch_zero(dw2, bytes, s));
+    return hip_status(launch_zero(dw13, 2 * bytes, s));
+  }
+  // (x is read by dw13 only)
+  if (!dy_perm || !offsets || !w13 || !w2 || !gu || (dw2 && !x_perm && (!x || !src_token)))
+    return MOE_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < moe_grouped_ffn_backward_workspace_size(max_rows, E_loc, H, I_loc, dt))
+    return MOE_ERR_WORKSPACE;
+  Carver c(ws);
+  void* h = c.take<char>((size_t)max_rows * I_loc * elt_bytes(dt));
+  void* dgu = c.take<char>((size_t)max_rows * I_loc * elt_bytes(dt) * 2);
+  const TrainFfn f{x_perm ? x_perm : x, x_perm ? nullptr : src_token, offsets, E_loc, max_rows, H,
+                   I_loc, dt, w13, w2, const_cast<float*>(gu), h};
+  return hip_status(launch_train_backward(f, dy_perm, dgu, dx_perm, dw13, dw2, s));
 }
 
 }  // extern "C"

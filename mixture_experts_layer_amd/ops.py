@@ -104,3 +104,40 @@ def moe_combine_backward(dy, dt, y_perm, y_perm_dt, dst_row, topk_w, T, k, H, dy
            ("dst_row", dst_row, "i", T * k), ("topk_w", topk_w, "f", T * k),
            ("dy_perm", dy_perm, y_perm_dt, 0), ("dtopk_w", dtopk_w, "f", T * k)),
           (dy, dt, y_perm, y_perm_dt, dst_row, topk_w, T, k, H, dy_perm, dtopk_w), stream)
+
+
+def moe_grouped_ffn_train_workspace_size(max_rows, E_loc, H, I_loc, dt) -> int:
+    from . import lib
+    return lib.moe_grouped_ffn_train_workspace_size(max_rows, E_loc, H, I_loc, dt)
+
+
+def moe_grouped_ffn_train(x_perm, x, src_token, offsets, E_loc, max_rows, H, I_loc, w13, w2, dt, gu,
+                          y_perm, ws, ws_bytes, stream=None):
+    n = max_rows * H
+    _call("moe_grouped_ffn_train",
+          (("x_perm", x_perm, dt, n), ("x", x, dt, 0),
+           ("src_token", src_token, "i", 0 if x_perm is not None else max_rows),
+           ("offsets", offsets, "i", E_loc + 1), ("w13", w13, dt, 2 * E_loc * I_loc * H),
+           ("w2", w2, dt, E_loc * I_loc * H), ("gu", gu, "f", 2 * max_rows * I_loc),
+           ("y_perm", y_perm, dt, n), ("ws", ws, "b", ws_bytes)),
+          (x_perm, x, src_token, offsets, E_loc, max_rows, H, I_loc, w13, w2, dt, gu, y_perm, ws,
+           ws_bytes), stream)
+
+
+def moe_grouped_ffn_backward_workspace_size(max_rows, E_loc, H, I_loc, dt) -> int:
+    from . import lib
+    return lib.moe_grouped_ffn_backward_workspace_size(max_rows, E_loc, H, I_loc, dt)
+
+
+def moe_grouped_ffn_backward(dy_perm, x_perm, x, src_token, offsets, E_loc, max_rows, H, I_loc, w13,
+                             w2, dt, gu, dx_perm, dw13, dw2, ws, ws_bytes, stream=None):
+    n, weights = max_rows * H, E_loc * I_loc * H
+    _call("moe_grouped_ffn_backward",
+          (("dy_perm", dy_perm, dt, n), ("x_perm", x_perm, dt, n), ("x", x, dt, 0),
+           ("src_token", src_token, "i", 0 if x_perm is not None else max_rows),
+           ("offsets", offsets, "i", E_loc + 1), ("w13", w13, dt, 2 * weights),
+           ("w2", w2, dt, weights), ("gu", gu, "f", 2 * max_rows * I_loc),
+           ("dx_perm", dx_perm, dt, n), ("dw13", dw13, dt, 2 * weights),
+           ("dw2", dw2, dt, weights), ("ws", ws, "b", ws_bytes)),
+          (dy_perm, x_perm, x, src_token, offsets, E_loc, max_rows, H, I_loc, w13, w2, dt, gu,
+           dx_perm, dw13, dw2, ws, ws_bytes), stream)

@@ -120,3 +120,49 @@ def test_the_binding_refuses_what_an_address_would_not_show():
         M.moe_rmsnorm(*args(x=torch.zeros(4, 512, dtype=torch.bfloat16)[:, ::2]))
     with pytest.raises(ValueError, match="fewer than"):
         M.moe_rmsnorm(*args(x=x[:3]))
+
+
+TRAIN = dict(x_perm=None, x=P, src_token=P, offsets=P, E_loc=4, max_rows=16, H=256, I_loc=128, w13=P, w2=P, dt=1,
+             gu=P, y_perm=P, ws=P, ws_bytes=1 << 20, stream=0)
+BACKWARD = dict(dy_perm=P, x_perm=None, x=P, src_token=P, offsets=P, E_loc=4, max_rows=16, H=256, I_loc=128, w13=P,
+                w2=P, dt=1, gu=P, dx_perm=P, dw13=P, dw2=P, ws=P, ws_bytes=1 << 20, stream=0)
+BLOCK_SHAPES = [
+    (dict(E_loc=0), INVALID), (dict(max_rows=-1), INVALID), (dict(H=0), INVALID), (dict(I_loc=0), INVALID),
+    (dict(E_loc=1025), UNSUPPORTED), (dict(H=40), UNSUPPORTED), (dict(I_loc=48), UNSUPPORTED),
+    (dict(H=65568), UNSUPPORTED), (dict(I_loc=65568), UNSUPPORTED), (dict(H=65536, I_loc=32768), UNSUPPORTED),
+]
+
+
+@pytest.mark.parametrize("kw,status", BLOCK_SHAPES + [
+    (dict(dt=2), INVALID), (dict(ws=None), WORKSPACE), (dict(ws_bytes=16 * 128 * 2 - 1), WORKSPACE),
+    (dict(x=None), INVALID), (dict(src_token=None), INVALID),
+] + [({n: None}, INVALID) for n in ("offsets", "w13", "w2", "gu", "y_perm")]
+  + [({n: MIS}, INVALID) for n in ("x_perm", "x", "src_token", "offsets", "w13", "w2", "gu", "y_perm", "ws")])
+def test_grouped_ffn_train_rejects(kw, status):
+    assert _st("moe_grouped_ffn_train", *dict(TRAIN, **kw).values()) == status
+
+
+@pytest.mark.parametrize("kw,status", BLOCK_SHAPES + [
+    (dict(dt=2), INVALID), (dict(ws=None), WORKSPACE), (dict(ws_bytes=3 * 16 * 128 * 2 - 1), WORKSPACE),
+    (dict(x=None), INVALID), (dict(src_token=None), INVALID), (dict(dw2=None), INVALID), (dict(dw13=None), INVALID),
+    (dict(dx_perm=None, dw13=None, dw2=None), INVALID), (dict(max_rows=0, dw13=None), INVALID),
+] + [({n: None}, INVALID) for n in ("dy_perm", "offsets", "w13", "w2", "gu")]
+  + [({n: MIS}, INVALID) for n in ("dy_perm", "x_perm", "x", "src_token", "offsets", "w13", "w2", "gu", "dx_perm",
+                                   "dw13", "dw2", "ws")])
+def test_grouped_ffn_backward_rejects(kw, status):
+    assert _st("moe_grouped_ffn_backward", *dict(BACKWARD, **kw).values()) == status
+
+
+def test_training_without_rows_needs_nothing_but_the_gradients():
+    none = dict(x=None, src_token=None, offsets=None, w13=None, w2=None, gu=None, ws=None, ws_bytes=0, max_rows=0)
+    assert _st("moe_grouped_ffn_train", *dict(TRAIN, y_perm=None, **none).values()) == 0
+    assert _st("moe_grouped_ffn_backward", *dict(BACKWARD, dy_perm=None, dw13=None, dw2=None, **none).values()) == 0
+
+
+def test_training_workspaces():
+    f, b = M.moe_grouped_ffn_train_workspace_size, M.moe_grouped_ffn_backward_workspace_size
+    assert f(65536, 128, 4096, 1536, 1) >= 65536 * 1536 * 2 and b(65536, 128, 4096, 1536, 1) >= 3 * 65536 * 1536 * 2
+    assert f(2 ** 31 - 1, 1, 16384, 65536, 0) > 2 ** 48         # sizes beyond 32 bits
+    for q in (f, b):
+        for bad in ((-1, 4, 256, 128, 1), (4, 0, 256, 128, 1), (4, 4, 256, 100, 1), (4, 4, 256, 128, 3)):
+            assert q(*bad) == 0
