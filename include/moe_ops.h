@@ -128,6 +128,27 @@ int moe_grouped_ffn_backward(const void* dy_perm, const void* x_perm, const void
                              int dt, const float* gu, void* dx_perm, void* dw13, void* dw2,
                              void* ws, size_t ws_bytes, void* stream);
 
+/*
+ * moe_grouped_ffn_mxfp8 -- moe_grouped_ffn on MXFP8 rows and weights.
+ *   g, u, y are products of the values the elements and scales stand for,
+ *   accumulated in float32 by the scaled matrix instructions; h = SiLU(g) * u
+ *   is brought to MXFP8 (blocks of 32 along I_loc) between the two products.
+ *
+ *   x8[*][H] with x_scale[*][MOE_MX_PITCH(H)], rows gathered by src_token, or
+ *   row r itself when src_token == NULL;
+ *   w13[E_loc][2*I_loc][H] with w13_scale[E_loc][2*I_loc][MOE_MX_PITCH(H)];
+ *   w2[E_loc][H][I_loc] with w2_scale[E_loc][H][MOE_MX_PITCH(I_loc)];
+ *   y_perm[max_rows][H] of dtype y_dt.  Elements must be finite and scale
+ *   bytes below 255.  Limits, offsets and sources as for
+ *   moe_grouped_ffn_train.
+ */
+size_t moe_grouped_ffn_mxfp8_workspace_size(int max_rows, int E_loc, int H, int I_loc);
+int moe_grouped_ffn_mxfp8(const void* x8, const uint8_t* x_scale, const int32_t* src_token,
+                          const int32_t* offsets, int E_loc, int max_rows, int H, int I_loc,
+                          const void* w13, const uint8_t* w13_scale, const void* w2,
+                          const uint8_t* w2_scale, void* y_perm, int y_dt, void* ws,
+                          size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

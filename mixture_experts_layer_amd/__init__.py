@@ -31,7 +31,8 @@ __all__ = [
     "moe_rmsnorm", "moe_rmsnorm_backward", "moe_rmsnorm_backward_workspace_size",
     "moe_combine_backward", "mx_pitch", "moe_grouped_ffn_train",
     "moe_grouped_ffn_train_workspace_size", "moe_grouped_ffn_backward",
-    "moe_grouped_ffn_backward_workspace_size",
+    "moe_grouped_ffn_backward_workspace_size", "moe_grouped_ffn_mxfp8",
+    "moe_grouped_ffn_mxfp8_workspace_size",
 ]
 
 _LIB = None
@@ -277,4 +278,5 @@ def debug_out(logits=None, topk_ids=None, topk_w=None, counts=None, offsets=None
 from .ops import (moe_rmsnorm, moe_rmsnorm_backward,  # noqa: E402
                   moe_rmsnorm_backward_workspace_size, moe_combine_backward, mx_pitch,
                   moe_grouped_ffn_train, moe_grouped_ffn_train_workspace_size,
-                  moe_grouped_ffn_backward, moe_grouped_ffn_backward_workspace_size)
+                  moe_grouped_ffn_backward, moe_grouped_ffn_backward_workspace_size,
+                  moe_grouped_ffn_mxfp8, moe_grouped_ffn_mxfp8_workspace_size)

@@ -98,6 +98,10 @@ _OPS_SIGS = {
                                          c_int, c_int, c_int, c_void_p, c_void_p, c_int, c_void_p,
                                          c_void_p, c_void_p, c_void_p, c_void_p, c_size_t,
                                          c_void_p]),
+    "moe_grouped_ffn_mxfp8_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int]),
+    "moe_grouped_ffn_mxfp8": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int,
+                                      c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                      c_int, c_void_p, c_size_t, c_void_p]),
 }
 # bytes of the device array moe_layer_static uses as its workspace
 STATIC_SCRATCH_BYTES = 64 << 20

@@ -28,7 +28,7 @@ LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libmoe_mi355x.so")
 SOURCES = ["abi.hip", "route.hip", "permute.hip", "ffn.hip", "combine.hip", "decode.hip",
            "dispatch.hip", "reshard.hip", "ops_abi.hip", "norm.hip",
-           "ffn_train.hip"]
+           "ffn_train.hip", "ffn_mxfp8.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

@@ -45,4 +45,22 @@ hipError_t launch_train_forward(const TrainFfn& f, void* y, hipStream_t st);
 hipError_t launch_train_backward(const TrainFfn& f, const void* dy, void* dgu, void* dx, void* dw13,
                                  void* dw2, hipStream_t st);
 
+// ffn_mxfp8.hip: the grouped SwiGLU experts on MXFP8 rows and weights.
+struct MxFfn {
+  const uint8_t* x8;        // rows of H, gathered by src_token (or null: permuted)
+  const uint8_t* x_scale;
+  const int32_t* src_token;
+  const int32_t* offsets;   // [E + 1]
+  int E, max_rows, H, I;
+  const uint8_t* w13;
+  const uint8_t* w13_scale;
+  const uint8_t* w2;
+  const uint8_t* w2_scale;
+  uint8_t* h8;              // [max_rows][I] and its scales, workspace
+  uint8_t* h_scale;
+  void* y;
+  int y_dt;
+};
+hipError_t launch_mx_ffn(const MxFfn& f, hipStream_t st);
+
 }  // namespace moe

@@ -151,4 +151,34 @@ int moe_grouped_ffn_backward(const void* dy_perm, const void* x_perm, const void
   return hip_status(launch_train_backward(f, dy_perm, dgu, dx_perm, dw13, dw2, s));
 }
 
+size_t moe_grouped_ffn_mxfp8_workspace_size(int max_rows, int E_loc, int H, int I_loc) {
+  if (check_block(max_rows, E_loc, H, I_loc) != MOE_OK) return 0;
+  const size_t rows = max_rows > 0 ? max_rows : 1;
+  return align_up(rows * I_loc) + align_up(rows * MOE_MX_PITCH(I_loc));
+}
+
+int moe_grouped_ffn_mxfp8(const void* x8, const uint8_t* x_scale, const int32_t* src_token,
+                          const int32_t* offsets, int E_loc, int max_rows, int H, int I_loc,
+                          const void* w13, const uint8_t* w13_scale, const void* w2,
+                          const uint8_t* w2_scale, void* y_perm, int y_dt, void* ws,
+                          size_t ws_bytes, void* stream) {
+  if (!valid_dt(y_dt)) return MOE_ERR_INVALID_ARG;
+  const int st = check_block(max_rows, E_loc, H, I_loc);
+  if (st) return st;
+  if (any_misaligned(x8, x_scale, src_token, offsets, w13, w13_scale, w2, w2_scale, y_perm, ws))
+    return MOE_ERR_INVALID_ARG;
+  if (max_rows == 0) return MOE_OK;
+  if (!x8 || !x_scale || !offsets || !w13 || !w13_scale || !w2 || !w2_scale || !y_perm)
+    return MOE_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < moe_grouped_ffn_mxfp8_workspace_size(max_rows, E_loc, H, I_loc))
+    return MOE_ERR_WORKSPACE;
+  Carver c(ws);
+  uint8_t* h8 = c.take<uint8_t>((size_t)max_rows * I_loc);
+  uint8_t* hs = c.take<uint8_t>((size_t)max_rows * MOE_MX_PITCH(I_loc));
+  const MxFfn f{static_cast<const uint8_t*>(x8), x_scale, src_token, offsets, E_loc, max_rows, H,
+                I_loc, static_cast<const uint8_t*>(w13), w13_scale,
+                static_cast<const uint8_t*>(w2), w2_scale, h8, hs, y_perm, y_dt};
+  return hip_status(launch_mx_ffn(f, static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -141,3 +141,21 @@ def moe_grouped_ffn_backward(dy_perm, x_perm, x, src_token, offsets, E_loc, max_
            ("dw2", dw2, dt, weights), ("ws", ws, "b", ws_bytes)),
           (dy_perm, x_perm, x, src_token, offsets, E_loc, max_rows, H, I_loc, w13, w2, dt, gu,
            dx_perm, dw13, dw2, ws, ws_bytes), stream)
+
+
+def moe_grouped_ffn_mxfp8_workspace_size(max_rows, E_loc, H, I_loc) -> int:
+    from . import lib
+    return lib.moe_grouped_ffn_mxfp8_workspace_size(max_rows, E_loc, H, I_loc)
+
+
+def moe_grouped_ffn_mxfp8(x8, x_scale, src_token, offsets, E_loc, max_rows, H, I_loc, w13,
+                          w13_scale, w2, w2_scale, y_perm, y_dt, ws, ws_bytes, stream=None):
+    rows, weights = 0 if src_token is not None else max_rows, E_loc * I_loc * H
+    _call("moe_grouped_ffn_mxfp8",
+          (("x8", x8, "8", rows * H), ("x_scale", x_scale, "b", rows * mx_pitch(H)),
+           ("src_token", src_token, "i", max_rows), ("offsets", offsets, "i", E_loc + 1),
+           ("w13", w13, "8", 2 * weights), ("w13_scale", w13_scale, "b", 2 * E_loc * I_loc * mx_pitch(H)),
+           ("w2", w2, "8", weights), ("w2_scale", w2_scale, "b", E_loc * H * mx_pitch(I_loc)),
+           ("y_perm", y_perm, y_dt, max_rows * H), ("ws", ws, "b", ws_bytes)),
+          (x8, x_scale, src_token, offsets, E_loc, max_rows, H, I_loc, w13, w13_scale, w2, w2_scale,
+           y_perm, y_dt, ws, ws_bytes), stream)

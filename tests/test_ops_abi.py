@@ -166,3 +166,25 @@ def test_training_workspaces():
     for q in (f, b):
         for bad in ((-1, 4, 256, 128, 1), (4, 0, 256, 128, 1), (4, 4, 256, 100, 1), (4, 4, 256, 128, 3)):
             assert q(*bad) == 0
+
+
+MX = dict(x8=P, x_scale=P, src_token=P, offsets=P, E_loc=4, max_rows=16, H=256, I_loc=128, w13=P, w13_scale=P, w2=P,
+          w2_scale=P, y_perm=P, y_dt=1, ws=P, ws_bytes=1 << 20, stream=0)
+
+
+@pytest.mark.parametrize("kw,status", BLOCK_SHAPES + [
+    (dict(y_dt=2), INVALID), (dict(ws=None), WORKSPACE), (dict(ws_bytes=16 * 128), WORKSPACE),
+] + [({n: None}, INVALID) for n in ("x8", "x_scale", "offsets", "w13", "w13_scale", "w2", "w2_scale", "y_perm")]
+  + [({n: MIS}, INVALID) for n in ("x8", "x_scale", "src_token", "offsets", "w13", "w13_scale", "w2", "w2_scale",
+                                   "y_perm", "ws")])
+def test_grouped_ffn_mxfp8_rejects(kw, status):
+    assert _st("moe_grouped_ffn_mxfp8", *dict(MX, **kw).values()) == status
+
+
+def test_mxfp8_workspace_and_no_rows():
+    q = M.moe_grouped_ffn_mxfp8_workspace_size
+    assert q(65536, 128, 4096, 1536) >= 65536 * (1536 + 48)
+    for bad in ((-1, 4, 256, 128), (4, 0, 256, 128), (4, 4, 256, 100), (4, 4, 65568, 32)):
+        assert q(*bad) == 0
+    none = {n: None for n in ("x8", "x_scale", "offsets", "w13", "w13_scale", "w2", "w2_scale", "y_perm", "ws")}
+    assert _st("moe_grouped_ffn_mxfp8", *dict(MX, max_rows=0, **none).values()) == 0
