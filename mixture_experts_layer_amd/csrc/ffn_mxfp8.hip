@@ -315,22 +315,32 @@ __global__ __launch_bounds__(C::NTHR, 1) void mx_tile_kernel(MxArgs a) {
 // ---------------------------------------------------------------------------
 // Direct kernel: 16 rows of one expert against weights streamed from memory
 // into the operands of v_mfma_scale_f32_16x16x128 (weights first, so
-// accumulator lane l holds columns 4 (l / 16) + i of row l % 16).  A block's
-// waves are CW groups of KW: each group takes its own output columns (SWIGLU:
-// 32 of h, two gate and two up tiles; else one tile of 16), and its waves
-// split the contraction and meet in LDS, in wave order.
+// accumulator lane l holds columns 4 (l / 16) + i of row l % 16).  A block's 8
+// waves are CW groups of KW = 8 / CW: each group takes its own output columns,
+// and its waves split the contraction and meet in LDS, in wave order.  A wave
+// keeps two batches of U = 2 steps of 128 in flight, one being multiplied.
+//   MX_UP      8 columns of h per group: 8 gate and the matching 8 up rows
+//              share an operand.  Blocks of 32 or more columns store h as
+//              MXFP8; narrower ones, which do not hold whole blocks of 32,
+//              store it in float32;
+//   MX_DOWN    16 columns of y per group, from MXFP8 h;
+//   MX_DOWN32  the same from float32 h, which the block brings to MXFP8 in LDS
+//              first (the same bits).
 // ---------------------------------------------------------------------------
-constexpr int MXD_U = 2;     // contraction steps of 128 whose loads are in flight together
+enum MxMode { MX_UP, MX_DOWN, MX_DOWN32 };
 
 __device__ __forceinline__ i32x4_v ld_nt16(const uint8_t* p) {
   return __builtin_nontemporal_load(reinterpret_cast<const i32x4_v*>(p));
 }
 
-template <bool SWIGLU, bool OUT_BF16, int CW, int KW>
-__global__ __launch_bounds__(CW * KW * 64) void mx_direct_kernel(MxArgs a) {
-  constexpr int NT = SWIGLU ? 4 : 1, COLS = SWIGLU ? 32 : 16, NTHR = CW * KW * 64;
-  constexpr int RED = NT * 4 * 65;              // floats of one wave's partial sums
-  __shared__ float red[CW * KW * RED];
+constexpr int MXD_MAX_LDS_K = 2048;    // contraction of MX_DOWN32: h rows in LDS
+
+template <int MODE, bool OUT_BF16, int CW>
+__global__ __launch_bounds__(512, 4) void mx_direct_kernel(MxArgs a) {
+  constexpr int COLS = MODE == MX_UP ? 8 : 16, U = 2, KW = 8 / CW, RED = 4 * 65;
+  constexpr bool QUANT = MODE == MX_UP && CW * COLS >= 32;
+  extern __shared__ __attribute__((aligned(16))) unsigned char hbuf[];   // MX_DOWN32
+  __shared__ float red[8 * RED];
   const int lane = threadIdx.x & 63;
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int cw = wid / KW, kw = wid % KW;
@@ -345,91 +355,144 @@ __global__ __launch_bounds__(CW * KW * 64) void mx_direct_kernel(MxArgs a) {
   const int n0 = nb + cw * COLS;
   const int lr = lane & 15, lg = lane >> 4;
   const int row = min(r0 + lr, r1 - 1);
-  const size_t src = a.src_token ? max(a.src_token[row], 0) : row;
-  const uint8_t* xa = a.A + src * a.K;
-  const uint8_t* xs = a.As + src * a.pitch;
-  const uint8_t* wp[NT];
-  const uint8_t* ws[NT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    // (a group past the last column re-reads row 0: N is a multiple of 32)
-    const int n = (n0 < a.N ? n0 : 0) + (SWIGLU ? (i & 1) * 16 + (i >> 1) * a.N : 0) + lr;
-    const size_t w = (size_t)t.e * a.b_rows + n;
-    wp[i] = a.B + w * a.K;
-    ws[i] = a.Bs + w * a.pitch;
-  }
-  f32x4_t acc[NT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  // the row's source is loaded here and turned into addresses only once the
+  // first weights are on their way
+  int src = a.src_token ? a.src_token[row] : row;
+  const uint8_t* xa = a.A;
+  const uint8_t* xs = a.As;
+  // (a group past the last column re-reads column 0; N is a multiple of 32)
+  const int nc = n0 < a.N ? n0 : 0;
+  const size_t wrow = (size_t)t.e * a.b_rows +
+                      (MODE == MX_UP ? nc + (lr & 7) + (lr >> 3) * a.N : nc + lr);
+  const uint8_t* wp = a.B + wrow * a.K;
+  const uint8_t* ws = a.Bs + wrow * a.pitch;
 
   const int steps = (a.K + 127) / 128;
   const int s0 = steps * kw / KW, s1 = steps * (kw + 1) / KW;
-  for (int s = s0; s < s1; s += MXD_U) {
-    i32x4_v w[MXD_U][NT][2], x[MXD_U][2];
-    int wsc[MXD_U][NT], xsc[MXD_U];
+  const int hp = steps * 128 + 16, hsp = steps * 4;       // MX_DOWN32: LDS rows of h, of scales
+  unsigned char* hscale = hbuf + 16 * hp;
+  // A batch's rows ride with its weights: loads return in order, so rows asked
+  // for after the next batch's weights would wait for those.
+  struct Batch {
+    i32x4_v w[U][2], x[U][2];
+    int wsc[U], xsc[U];
+  };
+  // (a step past this wave's share re-reads its last and is not multiplied;
+  // 16 bytes past the contraction's end re-read the row's first)
+  auto load_w = [&](Batch& b, int s) {
 #pragma unroll
-    for (int u = 0; u < MXD_U; ++u) {
-      // (a step past this wave's share re-reads its last and is not multiplied;
-      // 16 bytes past the contraction's end re-read the row's first)
-      const int st = min(s + u, s1 - 1);
+    for (int u = 0; u < U; ++u) {
+      const int st = min(s + u, max(s1, 1) - 1);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int k = st * 128 + h * 64 + lg * 16, ko = k < a.K ? k : 0;
-#pragma unroll
-        for (int i = 0; i < NT; ++i) w[u][i][h] = ld_nt16(wp[i] + ko);
-        x[u][h] = *reinterpret_cast<const i32x4_v*>(xa + ko);
+        const int k = st * 128 + h * 64 + lg * 16;
+        b.w[u][h] = ld_nt16(wp + (k < a.K ? k : 0));
       }
-#pragma unroll
-      for (int i = 0; i < NT; ++i) wsc[u][i] = *reinterpret_cast<const int*>(ws[i] + st * 4);
-      xsc[u] = *reinterpret_cast<const int*>(xs + st * 4);
+      b.wsc[u] = *reinterpret_cast<const int*>(ws + st * 4);
     }
+  };
+  auto load_x = [&](Batch& b, int s) {
 #pragma unroll
-    for (int u = 0; u < MXD_U; ++u) {
+    for (int u = 0; u < U; ++u) {
+      const int st = min(s + u, max(s1, 1) - 1);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int k = st * 128 + h * 64 + lg * 16;
+        if constexpr (MODE == MX_DOWN32)
+          b.x[u][h] = *reinterpret_cast<const i32x4_v*>(hbuf + lr * hp + k);
+        else
+          b.x[u][h] = *reinterpret_cast<const i32x4_v*>(xa + (k < a.K ? k : 0));
+      }
+      b.xsc[u] = *reinterpret_cast<const int*>(
+          MODE == MX_DOWN32 ? hscale + lr * hsp + st * 4 : xs + st * 4);
+    }
+  };
+  f32x4_t acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  auto multiply = [&](Batch& b, int s) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
       if (s + u >= s1) break;
       const int left = a.K - (s + u) * 128;
       if (left < 128) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (h * 64 + lg * 16 >= left) {
-            x[u][h] = i32x4_v{0, 0, 0, 0};
-#pragma unroll
-            for (int i = 0; i < NT; ++i) w[u][i][h] = i32x4_v{0, 0, 0, 0};
-          }
-        }
+        for (int h = 0; h < 2; ++h)
+          if (h * 64 + lg * 16 >= left) b.x[u][h] = b.w[u][h] = i32x4_v{0, 0, 0, 0};
       }
-      const i32x8_v xf = __builtin_shufflevector(x[u][0], x[u][1], 0, 1, 2, 3, 4, 5, 6, 7);
-      const int xsv = (int)((uint32_t)mx_valid_scales(xsc[u], left >> 5) >> (8 * lg));
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const i32x8_v wf = __builtin_shufflevector(w[u][i][0], w[u][i][1], 0, 1, 2, 3, 4, 5, 6, 7);
-        const int wsv = (int)((uint32_t)mx_valid_scales(wsc[u][i], left >> 5) >> (8 * lg));
-        acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf, acc[i], 0, 0, 0, wsv, 0,
-                                                                  xsv);
-      }
+      const i32x8_v xf = __builtin_shufflevector(b.x[u][0], b.x[u][1], 0, 1, 2, 3, 4, 5, 6, 7);
+      const i32x8_v wf = __builtin_shufflevector(b.w[u][0], b.w[u][1], 0, 1, 2, 3, 4, 5, 6, 7);
+      const int xsv = (int)((uint32_t)mx_valid_scales(b.xsc[u], left >> 5) >> (8 * lg));
+      const int wsv = (int)((uint32_t)mx_valid_scales(b.wsc[u], left >> 5) >> (8 * lg));
+      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf, acc, 0, 0, 0, wsv, 0, xsv);
     }
+  };
+  Batch b0, b1;
+  load_w(b0, s0);
+  if constexpr (MODE == MX_DOWN32) {
+    // the rows' h to MXFP8: 8 elements per thread, four threads to a block of
+    // 32; rows past the tile and steps past the contraction are zeros
+    const int n8 = steps * 16;
+    for (int i = threadIdx.x; i < 16 * n8; i += 512) {
+      const int m = i / n8, c = i - m * n8;
+      float f[8];
+      if (r0 + m < r1 && c * 8 < a.K) {
+        Chunk<false> v;
+        v.load(a.A + (size_t)(r0 + m) * a.K * 4, c);
+        v.get(f);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = 0.f;
+      }
+      float mx = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(f[e]));
+      const uint32_t b8 = mx_scale_byte(quad_max(mx));
+      const float k = mx_inv_scale(b8);
+      *reinterpret_cast<uint2*>(hbuf + m * hp + c * 8) =
+          make_uint2(mx_pack4(f[0] * k, f[1] * k, f[2] * k, f[3] * k),
+                     mx_pack4(f[4] * k, f[5] * k, f[6] * k, f[7] * k));
+      if ((c & 3) == 0) hscale[m * hsp + (c >> 2)] = (unsigned char)b8;
+    }
+    __syncthreads();
+  } else {
+    asm volatile("" : "+v"(src)::"memory");      // the wait for the source lands here
+    xa = a.A + (size_t)max(src, 0) * a.K;
+    xs = a.As + (size_t)max(src, 0) * a.pitch;
+  }
+  load_x(b0, s0);
+  for (int s = s0; s < s1; s += 2 * U) {
+    if (s + U < s1) {
+      load_w(b1, s + U);
+      load_x(b1, s + U);
+    }
+    multiply(b0, s);
+    if (s + U >= s1) break;
+    if (s + 2 * U < s1) {
+      load_w(b0, s + 2 * U);
+      load_x(b0, s + 2 * U);
+    }
+    multiply(b1, s + U);
   }
 
 #pragma unroll
-  for (int i = 0; i < NT; ++i)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) red[wid * RED + (i * 4 + q) * 65 + lane] = acc[i][q];
+  for (int q = 0; q < 4; ++q) red[wid * RED + q * 65 + lane] = acc[q];
   __syncthreads();
   // outputs of the block: 16 rows x CW * COLS columns, columns fastest
   constexpr int BC = CW * COLS;
-  for (int o = threadIdx.x; o < 16 * BC; o += NTHR) {
+  for (int o = threadIdx.x; o < 16 * BC; o += 512) {
     const int m = o / BC, c = o - m * BC, g = c / COLS, n = c - g * COLS;
-    const int at = (n & 3) * 65 + m + 16 * ((n & 15) >> 2) + (SWIGLU ? (n >> 4) * 4 * 65 : 0);
+    const int at = (n & 3) * 65 + m + 16 * (n >> 2);
     float v = 0.f, u = 0.f;
 #pragma unroll
     for (int k = 0; k < KW; ++k) {
       const float* p = red + (g * KW + k) * RED + at;
       v += p[0];
-      if (SWIGLU) u += p[SWIGLU ? 8 * 65 : 0];
+      if (MODE == MX_UP) u += p[MODE == MX_UP ? 32 : 0];   // the up sums lie 32 lanes on
     }
     const bool live = r0 + m < r1 && nb + c < a.N;
-    if constexpr (SWIGLU) {
-      // 32 consecutive lanes hold a row's block (16 * BC and NTHR are
-      // multiples of 64, so whole waves take part)
+    const size_t yi = (size_t)(r0 + m) * a.N + nb + c;
+    if constexpr (QUANT) {
+      // 32 consecutive lanes hold a row's block (BC is a multiple of 32, and
+      // whole waves take part)
       const float h = silu_fast(v) * u;
       float mx = fabsf(h);
 #pragma unroll
@@ -437,13 +500,12 @@ __global__ __launch_bounds__(CW * KW * 64) void mx_direct_kernel(MxArgs a) {
       const uint32_t b8 = mx_scale_byte(mx);
       const float hk = h * mx_inv_scale(b8);
       if (live) {
-        static_cast<uint8_t*>(a.Y)[(size_t)(r0 + m) * a.N + nb + c] =
-            (uint8_t)(mx_pack4(hk, hk, hk, hk) & 0xff);
+        static_cast<uint8_t*>(a.Y)[yi] = (uint8_t)(mx_pack4(hk, hk, hk, hk) & 0xff);
         if ((c & 31) == 0) a.Ys[(size_t)(r0 + m) * a.out_pitch + ((nb + c) >> 5)] = (uint8_t)b8;
       }
     } else if (live) {
-      const size_t yi = (size_t)(r0 + m) * a.N + nb + c;
-      if (OUT_BF16) static_cast<bf16_t*>(a.Y)[yi] = (bf16_t)(cvt_bf16x2(v, v) & 0xffff);
+      if constexpr (MODE == MX_UP) static_cast<float*>(a.Y)[yi] = silu_fast(v) * u;
+      else if (OUT_BF16) static_cast<bf16_t*>(a.Y)[yi] = (bf16_t)(cvt_bf16x2(v, v) & 0xffff);
       else static_cast<float*>(a.Y)[yi] = v;
     }
   }
@@ -473,47 +535,94 @@ static hipError_t launch_mx_tile_t(const MxArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <bool SWIGLU, bool OUT_BF16, int CW, int KW>
+template <int MODE, bool OUT_BF16, int CW>
 static hipError_t launch_mx_direct_t(const MxArgs& a, hipStream_t st) {
-  constexpr int cols = CW * (SWIGLU ? 32 : 16);
+  constexpr int cols = CW * (MODE == MX_UP ? 8 : 16);
   const long long grid = mx_row_tiles(a.max_rows, a.E, 16) * ((a.N + cols - 1) / cols);
   if (grid > INT32_MAX) return hipErrorInvalidValue;
-  mx_direct_kernel<SWIGLU, OUT_BF16, CW, KW><<<(unsigned)grid, CW * KW * 64, 0, st>>>(a);
+  int lds = 0;
+  if (MODE == MX_DOWN32) {
+    const int steps = (a.K + 127) / 128;
+    lds = 16 * (steps * 128 + 16) + 16 * steps * 4;
+  }
+  mx_direct_kernel<MODE, OUT_BF16, CW><<<(unsigned)grid, 512, lds, st>>>(a);
   return hipGetLastError();
 }
-
-enum MxPath { MX_DIRECT, MX_MED, MX_BIG };
-static MxPath mx_path(int max_rows, int E) {
+// Which kernel takes each product.  Measured on MI355X, replayed from a graph
+// (us; up kernel / down kernel; d<n>: direct with n column groups per block):
+//   I/P = 192, 8 experts x 1 row:     d1/d8 11.4  d2/d8 13.7  d4/d8 20.1  tiles 40.2
+//     49 experts:                     d1/d8 42.4  d2/d8 44.8  tiles 59.2
+//     87 experts:                     d1/d8 69.9  tiles/d8 64.4  tiles 74.8
+//   I = 1536, 8 experts:              d2/d8 44.9  d1/d8 45.9  tiles 51.3
+//     15 experts:                     d2/d8 73.8  tiles 67.2
+//   I = 2048, H = 7168, 8 experts:    d4/tiles 88.7  d2/d8 98.4  tiles 110
+//     13 experts:                     d2/d8 155   tiles 138
+//   I = 14336, 2 experts:             tiles/d2 74.3  tiles/d8 147  d4/d8 173  tiles 207
+//     8 experts, 4 rows each:         tiles/d2 345   tiles 367
+// The tiled kernel streams faster (5.1 against 4.1 TB/s) but needs a block of
+// 1 MB of weights per CU; a contraction of one or two steps gains nothing from
+// its pipeline; and the direct kernel's 16-row tiles read the weights again
+// for every 16 rows.
+enum MxKernel { MX_K_DIRECT, MX_K_MED, MX_K_BIG };
+struct MxPlan {
+  MxKernel up, down;
+  int cw_up, cw_down;     // direct kernels: column groups per block
+  bool h_float;           // h in float32 between the products
+};
+static MxPlan mx_plan(int max_rows, int E, int H, int I) {
+  MxPlan p{};
   const int mean = (max_rows + E - 1) / E;
-  return mean <= 8 ? MX_DIRECT : mean < 384 ? MX_MED : MX_BIG;
+  // experts with rows, were every row's expert drawn alike, and their row tiles
+  const double touched = E * (1.0 - __builtin_pow(1.0 - 1.0 / E, (double)max_rows));
+  const double tiles = std::max(touched, max_rows / 128.0);
+  const MxKernel tiled = mean < 384 ? MX_K_MED : MX_K_BIG;
+  const bool few = mean <= 64;
+  p.up = few && tiles * ((I + 127) / 128) < 160 ? MX_K_DIRECT : tiled;
+  p.down = few && (I <= 256 || tiles * ((H + 255) / 256) < 256) ? MX_K_DIRECT : tiled;
+  const int steps = (I + 127) / 128;
+  p.cw_down = steps <= 16 ? 8 : steps <= 48 ? 4 : 2;
+  p.cw_up = 4;
+  if (p.up == MX_K_DIRECT && p.down == MX_K_DIRECT && I <= MXD_MAX_LDS_K)
+    p.cw_up = touched * (I / 8) < 1024 ? 1 : 2;
+  p.h_float = p.up == MX_K_DIRECT && p.cw_up < 4;
+  return p;
 }
 
 template <bool SWIGLU, bool OUT_BF16>
-static hipError_t launch_mx(const MxArgs& a, MxPath path, hipStream_t st) {
-  if (path == MX_DIRECT) {
-    if constexpr (SWIGLU) return launch_mx_direct_t<true, true, 1, 8>(a, st);
-    else return launch_mx_direct_t<false, OUT_BF16, 4, 2>(a, st);
-  }
+static hipError_t launch_mx_tiled(const MxArgs& a, MxKernel k, hipStream_t st) {
   if constexpr (SWIGLU) {
     if (a.src_token)
-      return path == MX_BIG ? launch_mx_tile_t<MxBig, true, true, true>(a, st)
-                            : launch_mx_tile_t<MxMed, true, true, true>(a, st);
+      return k == MX_K_BIG ? launch_mx_tile_t<MxBig, true, true, true>(a, st)
+                           : launch_mx_tile_t<MxMed, true, true, true>(a, st);
   }
-  return path == MX_BIG ? launch_mx_tile_t<MxBig, SWIGLU, OUT_BF16, false>(a, st)
-                        : launch_mx_tile_t<MxMed, SWIGLU, OUT_BF16, false>(a, st);
+  return k == MX_K_BIG ? launch_mx_tile_t<MxBig, SWIGLU, OUT_BF16, false>(a, st)
+                       : launch_mx_tile_t<MxMed, SWIGLU, OUT_BF16, false>(a, st);
 }
 
+template <bool OUT_BF16>
+static hipError_t launch_mx_down(const MxArgs& a, const MxPlan& p, hipStream_t st) {
+  if (p.down != MX_K_DIRECT) return launch_mx_tiled<false, OUT_BF16>(a, p.down, st);
+  if (p.h_float) return launch_mx_direct_t<MX_DOWN32, OUT_BF16, 8>(a, st);   // I is short there
+  return p.cw_down == 8   ? launch_mx_direct_t<MX_DOWN, OUT_BF16, 8>(a, st)
+         : p.cw_down == 4 ? launch_mx_direct_t<MX_DOWN, OUT_BF16, 4>(a, st)
+                          : launch_mx_direct_t<MX_DOWN, OUT_BF16, 2>(a, st);
+}
+
+bool mx_h_is_float(int max_rows, int E, int H, int I) { return mx_plan(max_rows, E, H, I).h_float; }
+
 hipError_t launch_mx_ffn(const MxFfn& f, hipStream_t st) {
-  const MxPath path = mx_path(f.max_rows, f.E);
+  const MxPlan p = mx_plan(f.max_rows, f.E, f.H, f.I);
   const int pH = (f.H + 127) / 128 * 4, pI = (f.I + 127) / 128 * 4;
   const MxArgs up{f.x8, f.x_scale, f.src_token, f.offsets, f.E, f.max_rows, f.w13, f.w13_scale,
                   f.H, f.I, 2 * f.I, pH, pI, f.h8, f.h_scale};
-  hipError_t err = launch_mx<true, true>(up, path, st);
+  const hipError_t err = p.up != MX_K_DIRECT ? launch_mx_tiled<true, true>(up, p.up, st)
+                         : p.cw_up == 1      ? launch_mx_direct_t<MX_UP, true, 1>(up, st)
+                         : p.cw_up == 2      ? launch_mx_direct_t<MX_UP, true, 2>(up, st)
+                                             : launch_mx_direct_t<MX_UP, true, 4>(up, st);
   if (err != hipSuccess) return err;
   const MxArgs down{f.h8, f.h_scale, nullptr, f.offsets, f.E, f.max_rows, f.w2, f.w2_scale,
                     f.I, f.H, f.H, pI, 0, f.y, nullptr};
-  return f.y_dt == 1 ? launch_mx<false, true>(down, path, st)
-                     : launch_mx<false, false>(down, path, st);
+  return f.y_dt == 1 ? launch_mx_down<true>(down, p, st) : launch_mx_down<false>(down, p, st);
 }
 
 }  // namespace moe

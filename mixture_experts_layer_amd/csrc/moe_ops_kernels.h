@@ -56,11 +56,13 @@ struct MxFfn {
   const uint8_t* w13_scale;
   const uint8_t* w2;
   const uint8_t* w2_scale;
-  uint8_t* h8;              // [max_rows][I] and its scales, workspace
+  uint8_t* h8;              // workspace: h [max_rows][I] in e4m3 and its scales,
+                            // or in float32 where mx_h_is_float
   uint8_t* h_scale;
   void* y;
   int y_dt;
 };
+bool mx_h_is_float(int max_rows, int E, int H, int I);
 hipError_t launch_mx_ffn(const MxFfn& f, hipStream_t st);
 
 }  // namespace moe

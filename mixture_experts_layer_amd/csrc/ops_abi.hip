@@ -154,6 +154,7 @@ int moe_grouped_ffn_backward(const void* dy_perm, const void* x_perm, const void
 size_t moe_grouped_ffn_mxfp8_workspace_size(int max_rows, int E_loc, int H, int I_loc) {
   if (check_block(max_rows, E_loc, H, I_loc) != MOE_OK) return 0;
   const size_t rows = max_rows > 0 ? max_rows : 1;
+  if (mx_h_is_float(max_rows, E_loc, H, I_loc)) return align_up(rows * I_loc * 4);
   return align_up(rows * I_loc) + align_up(rows * MOE_MX_PITCH(I_loc));
 }
 
@@ -173,7 +174,7 @@ int moe_grouped_ffn_mxfp8(const void* x8, const uint8_t* x_scale, const int32_t*
   if (!ws || ws_bytes < moe_grouped_ffn_mxfp8_workspace_size(max_rows, E_loc, H, I_loc))
     return MOE_ERR_WORKSPACE;
   Carver c(ws);
-  uint8_t* h8 = c.take<uint8_t>((size_t)max_rows * I_loc);
+  uint8_t* h8 = c.take<uint8_t>((size_t)max_rows * I_loc);   // (float32 h leaves hs unused)
   uint8_t* hs = c.take<uint8_t>((size_t)max_rows * MOE_MX_PITCH(I_loc));
   const MxFfn f{static_cast<const uint8_t*>(x8), x_scale, src_token, offsets, E_loc, max_rows, H,
                 I_loc, static_cast<const uint8_t*>(w13), w13_scale,

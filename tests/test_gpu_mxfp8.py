@@ -198,3 +198,16 @@ def test_graph_replays():
         torch.cuda.synchronize()
         assert torch.equal(got, y)
     b.verify(y)
+
+
+# one case for each pair of kernels that the two products may take: wide h
+# (columns in groups of 32, contraction split over 2 and 4 waves), h in float32
+# from groups of 8 and 16 columns, direct up with tiled down, tiled up with
+# direct down
+@pytest.mark.parametrize("counts,H,I", [
+    ([1, 0, 3], 64, 2080), ([2, 1], 96, 6240), ([8] * 9, 256, 1056), ([1, 2], 4096, 192),
+    ([1, 2, 0, 1] * 18, 1376, 288), ([2, 1, 3] * 32, 160, 224), ([70], 256, 128), ([33, 50], 288, 2112)])
+def test_each_choice_of_kernels(counts, H, I):
+    b = Block(counts, H, I, seed=27)
+    for y_dt in (BF16, F32):
+        b.verify(b.run(y_dt))
