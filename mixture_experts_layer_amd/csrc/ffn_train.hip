@@ -33,9 +33,15 @@
 
 namespace moe {
 
-typedef short s16x4_t __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
-typedef const __attribute__((address_space(4))) int32_t* const_i32_t;
+typedef uint32_t u32x2_v __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4_v __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ bf16x8_t tr_join(u32x2_v lo, u32x2_v hi) {
+  return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3));
+}
+
+__device__ __forceinline__ uint32_t lds_addr(const unsigned char* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) unsigned char*)p;
+}
 
 enum Epilogue { EPI_STORE, EPI_SWIGLU, EPI_DSWIGLU };
 
@@ -44,7 +50,7 @@ struct GemmArgs {
   const bf16_t* B;
   long long lda, ldb;         // elements between memory rows
   long long b_stride;         // elements between experts' B (weights)
-  const int32_t* src_token;   // gathered operand: A by rows, or B in a weight gradient
+  const int32_t* src_token;   // GATHER: row r of A is row src_token[r]
   const int32_t* offsets;
   int E, max_rows;
   int M, N, K;                // rows of a weight gradient; output columns; contraction (weights)
@@ -54,15 +60,13 @@ struct GemmArgs {
   long long out_stride;       // elements between experts' outputs (weight gradients)
   bf16_t* out2;               // EPI_SWIGLU, EPI_DSWIGLU: h [rows][N]
   float* gu;                  // [rows][2 N] of EPI_SWIGLU (written) and EPI_DSWIGLU (read)
-  int group;                  // column tiles that run side by side
 };
 
 // Tile shape: TM x TN outputs, STAGES buffers of 64 along the contraction,
 // WM x WN waves of (TM / WM) x (TN / WN) outputs each.
-template <int TM_, int TN_, int STAGES_, int WM_, int WN_, int MINB_>
+template <int TM_, int TN_, int TK_, int STAGES_, int WM_, int WN_>
 struct GemmCfg {
-  static constexpr int TM = TM_, TN = TN_, STAGES = STAGES_, WM = WM_, WN = WN_, MINB = MINB_;
-  static constexpr int TK = 64;
+  static constexpr int TM = TM_, TN = TN_, TK = TK_, STAGES = STAGES_, WM = WM_, WN = WN_;
   static constexpr int NW = WM * WN, NTHR = NW * 64;
   static constexpr int WTM = TM / WM, WTN = TN / WN, MFM = WTM / 32, MFN = WTN / 32;
   static constexpr int ABYTES = TM * TK * 2, BBYTES = TN * TK * 2, SBYTES = ABYTES + BBYTES;
@@ -74,67 +78,80 @@ struct GemmCfg {
   static_assert(LDS <= 160 * 1024, "LDS per block");
 };
 
-// KC tile [row][64]: 8 chunks of 16 bytes per row, chunk c of row r at
-// c ^ (r / 2 % 8): the 16 lanes that read one chunk of 16 rows then cover the
-// banks once.
-__device__ __forceinline__ int kc_swz(int r) { return (r >> 1) & 7; }
+// KC tile [row][TK]: 16-byte chunks, chunk c of row r at c ^ (r / 2 % 8) for 8
+// chunks per row, c ^ (r / 4 % 4) for 4: the 16 lanes that read one chunk of 16
+// rows then cover the banks once.
+template <int TK>
+__device__ __forceinline__ int kc_swz(int r) {
+  return TK == 64 ? (r >> 1) & 7 : (r >> 2) & 3;
+}
 // MC tile [k][TN or TM columns]: 64-byte segments, segment s of row k at
 // s ^ (k % 4): the four k-rows of 64 bytes that half a wave reads lie in
 // different quarters of the banks.
 __device__ __forceinline__ int mc_chunk(int k, int chunk) { return chunk ^ ((k & 3) << 2); }
 
+// Transposing LDS reads of N fragments (32 columns x 16 k-rows each, ROW bytes
+// per k-row) at LDS addresses at[] + OFF.  One asm block that ends with the
+// wait for what it reads: the compiler's own bookkeeping makes the builtin
+// form wait for every LDS-direct load in flight, which emptied the load
+// pipeline at each chunk (the products by W2 and W13 ran 20% below the
+// transpose-free ones).  The other wave of the SIMD multiplies meanwhile.
+template <int OFF, int ROW>
+__device__ __forceinline__ void tr_read(const uint32_t (&at)[2], bf16x8_t (&f)[2]) {
+  u32x2_v a0, a1, b0, b1;
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %4 offset:%6\n\t"
+      "ds_read_b64_tr_b16 %1, %4 offset:%7\n\t"
+      "ds_read_b64_tr_b16 %2, %5 offset:%6\n\t"
+      "ds_read_b64_tr_b16 %3, %5 offset:%7\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(a0), "=&v"(a1), "=&v"(b0), "=&v"(b1)
+      : "v"(at[0]), "v"(at[1]), "n"(OFF), "n"(OFF + 4 * ROW)
+      : "memory");
+  f[0] = tr_join(a0, a1);
+  f[1] = tr_join(b0, b1);
+}
+template <int OFF, int ROW>
+__device__ __forceinline__ void tr_read(const uint32_t (&at)[4], bf16x8_t (&f)[4]) {
+  u32x2_v a0, a1, b0, b1, c0, c1, d0, d1;
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %8 offset:%12\n\t"
+      "ds_read_b64_tr_b16 %1, %8 offset:%13\n\t"
+      "ds_read_b64_tr_b16 %2, %9 offset:%12\n\t"
+      "ds_read_b64_tr_b16 %3, %9 offset:%13\n\t"
+      "ds_read_b64_tr_b16 %4, %10 offset:%12\n\t"
+      "ds_read_b64_tr_b16 %5, %10 offset:%13\n\t"
+      "ds_read_b64_tr_b16 %6, %11 offset:%12\n\t"
+      "ds_read_b64_tr_b16 %7, %11 offset:%13\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(a0), "=&v"(a1), "=&v"(b0), "=&v"(b1), "=&v"(c0), "=&v"(c1), "=&v"(d0), "=&v"(d1)
+      : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "n"(OFF), "n"(OFF + 4 * ROW)
+      : "memory");
+  f[0] = tr_join(a0, a1);
+  f[1] = tr_join(b0, b1);
+  f[2] = tr_join(c0, c1);
+  f[3] = tr_join(d0, d1);
+}
+
+// One output tile: rows [r0, r1) (of expert e; in a weight gradient, rows of the
+// parameter), columns from n0 on, a contraction of K (from memory row krow0 on).
 template <class C, bool WGRAD, bool BKC, int EPI, bool GATHER>
-__global__ __launch_bounds__(C::NTHR, C::MINB) void train_gemm_kernel(GemmArgs a) {
+__device__ __forceinline__ void gemm_tile(const GemmArgs& a, unsigned char* smem, int e, int r0,
+                                          int r1, int n0, int K, int krow0) {
   constexpr bool AKC = !WGRAD;
-  static_assert(!WGRAD || (!BKC && EPI == EPI_STORE), "weight gradients contract over rows");
-  extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
+  static_assert(!WGRAD || (!BKC && EPI == EPI_STORE && !GATHER), "weight gradients");
   const int lane = threadIdx.x & 63;
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   constexpr int COLS = EPI == EPI_SWIGLU ? C::TN / 2 : C::TN;
-  const int NT = (a.N + COLS - 1) / COLS;
-
-  // ---- the block's expert, row range [r0, r1), column n0, contraction K
-  int b = blockIdx.x, e, r0, r1, n_t, K, krow0 = 0;
-  if constexpr (WGRAD) {
-    const int MT = (a.M + C::TM - 1) / C::TM, n_active = a.E * MT * NT, per = n_active >> 3;
-    if (b < per * 8) b = (b & 7) * per + (b >> 3);      // contiguous numbers share an XCD's L2
-    e = b / (MT * NT);
-    const int li = b - e * MT * NT;
-    const int g = li / (MT * a.group), rem = li - g * MT * a.group;
-    const int Gc = min(a.group, NT - g * a.group);
-    const int m_t = rem / Gc;
-    n_t = g * a.group + (rem - m_t * Gc);
-    r0 = m_t * C::TM;
-    r1 = min(r0 + C::TM, a.M);
-    const int o = a.offsets[e], end = a.offsets[e + 1];
-    K = expert_tiles(o, end, 1, a.max_rows);
-    krow0 = K ? o : 0;
-  } else {
-    TileScan scan;
-    scan.init(a.offsets, a.E, C::TM, a.max_rows);
-    const int n_active = scan.total * NT, per = n_active >> 3;
-    if (b >= n_active) return;
-    if (b < per * 8) b = (b & 7) * per + (b >> 3);
-    const RowTile t = scan.find(a.offsets, a.E, C::TM, a.max_rows, b / NT);
-    e = t.e;
-    const int te = (t.end - t.off + C::TM - 1) / C::TM, li = b - t.first * NT;
-    const int g = li / (te * a.group), rem = li - g * te * a.group;
-    const int Gc = min(a.group, NT - g * a.group);
-    const int m_t = rem / Gc;
-    n_t = g * a.group + (rem - m_t * Gc);
-    r0 = t.off + m_t * C::TM;
-    r1 = min(r0 + C::TM, t.end);
-    K = a.K;
-  }
-  const int n0 = n_t * COLS;
   const bf16_t* Be = WGRAD ? a.B : a.B + (size_t)e * a.b_stride;
 
   // ---- lanes' sources.  Rows and columns past the end read the last one (or
   // the first column): their products are not stored.
-  // KC: the chunk this lane loads of its row, the same for every load
-  // (rows step by 64); row wid * 8 + lane / 8 of the first
+  // KC: one load covers KRPI rows; the chunk this lane loads of its row is the
+  // same for every load (rows step by NW * KRPI, a multiple of 16)
+  constexpr int KCPR = C::TK / 8, KRPI = 64 / KCPR;
   static_assert(C::NW == 8, "chunk of a lane");
-  const int kchunk = (lane & 7) ^ kc_swz(wid * 8 + (lane >> 3));
+  const int kchunk = (lane % KCPR) ^ kc_swz<C::TK>(wid * KRPI + lane / KCPR);
   const unsigned char* abase;
   const unsigned char* bbase;
   uint32_t ao[C::ALOADS], bo[C::BLOADS];
@@ -143,7 +160,7 @@ __global__ __launch_bounds__(C::NTHR, C::MINB) void train_gemm_kernel(GemmArgs a
     abase = reinterpret_cast<const unsigned char*>(a.A + (size_t)r0 * a.lda);
 #pragma unroll
     for (int j = 0; j < C::ALOADS; ++j) {
-      const int rt = (wid + C::NW * j) * 8 + (lane >> 3);
+      const int rt = (wid + C::NW * j) * KRPI + lane / KCPR;
       const int row = min(r0 + rt, r1 - 1);
       ao[j] = (uint32_t)((size_t)(row - r0) * a.lda * 2 + kchunk * 16);
       if constexpr (GATHER)
@@ -165,7 +182,7 @@ __global__ __launch_bounds__(C::NTHR, C::MINB) void train_gemm_kernel(GemmArgs a
     bbase = reinterpret_cast<const unsigned char*>(Be);
 #pragma unroll
     for (int j = 0; j < C::BLOADS; ++j) {
-      const int rt = (wid + C::NW * j) * 8 + (lane >> 3);
+      const int rt = (wid + C::NW * j) * KRPI + lane / KCPR;
       int row;
       if (EPI == EPI_SWIGLU)
         row = rt < COLS ? min(n0 + rt, a.N - 1) : a.up_off + min(n0 + rt - COLS, a.N - 1);
@@ -174,30 +191,16 @@ __global__ __launch_bounds__(C::NTHR, C::MINB) void train_gemm_kernel(GemmArgs a
       bo[j] = (uint32_t)((size_t)row * a.ldb * 2 + kchunk * 16);
     }
   } else {
-    bbase = reinterpret_cast<const unsigned char*>(WGRAD ? Be + (GATHER ? 0 : (size_t)krow0 * a.ldb)
-                                                         : Be);
+    bbase = reinterpret_cast<const unsigned char*>(WGRAD ? Be + (size_t)krow0 * a.ldb : Be);
 #pragma unroll
     for (int j = 0; j < C::BLOADS; ++j) {
       const int k = (wid + C::NW * j) * BRPI + lane / BCPR;
       const int col = n0 + mc_chunk(k, lane % BCPR) * 8;
-      bo[j] = (uint32_t)((GATHER ? 0 : (size_t)k * a.ldb * 2) + (col < a.N ? col : 0) * 2);
+      bo[j] = (uint32_t)((size_t)k * a.ldb * 2 + (col < a.N ? col : 0) * 2);
     }
   }
 
   const int nk = (K + C::TK - 1) / C::TK;
-  // gathered rows of a weight gradient: the sources of the next chunk's rows,
-  // uniform in the wave (scalar loads), one chunk ahead of their use
-  int tok[WGRAD && GATHER ? C::BLOADS : 1][BRPI];
-  auto load_tok = [&](int ks) {
-    if constexpr (WGRAD && GATHER) {
-      const_i32_t st = (const_i32_t)(uintptr_t)(a.src_token + krow0);
-#pragma unroll
-      for (int j = 0; j < C::BLOADS; ++j)
-#pragma unroll
-        for (int p = 0; p < BRPI; ++p)
-          tok[j][p] = st[min(ks * C::TK + (wid + C::NW * j) * BRPI + p, K - 1)];
-    }
-  };
   // `part`: the last chunk holds fewer than TK; what lies past the end re-reads
   // valid rows or columns (and is zeroed in LDS before the products)
   auto issue_as = [&](int ks, int buf, auto part_c) {
@@ -212,6 +215,8 @@ __global__ __launch_bounds__(C::NTHR, C::MINB) void train_gemm_kernel(GemmArgs a
     if constexpr (AKC) {
 #pragma unroll
       for (int j = 0; j < C::ALOADS; ++j) {
+        // (counted waits, beyond two stages, need them all)
+        if (C::STAGES == 2 && j > 0 && C::NW * KRPI * j >= r1 - r0) break;
         if constexpr (GATHER)
           __builtin_amdgcn_global_load_lds((gbl_void_t*)(ap[j] + (size_t)ks * (C::TK * 2) - kback),
                                            (lds_void_t*)(sa + C::NW * j * 1024), 16, 0, 0);
@@ -232,17 +237,6 @@ __global__ __launch_bounds__(C::NTHR, C::MINB) void train_gemm_kernel(GemmArgs a
       for (int j = 0; j < C::BLOADS; ++j)
         buffer_load_lds16(bbase, 0xffffffffu, sb + C::NW * j * 1024, bo[j] - kback,
                           (uint32_t)ks * (C::TK * 2));
-    } else if constexpr (WGRAD && GATHER) {
-#pragma unroll
-      for (int j = 0; j < C::BLOADS; ++j) {
-        int t = tok[j][0];
-#pragma unroll
-        for (int p = 1; p < BRPI; ++p) t = lane / BCPR == p ? tok[j][p] : t;
-        __builtin_amdgcn_global_load_lds(
-            (gbl_void_t*)(bbase + (size_t)max(t, 0) * a.ldb * 2 + bo[j]),
-            (lds_void_t*)(sb + C::NW * j * 1024), 16, 0, 0);
-      }
-      load_tok(ks + 1);
     } else {
       const unsigned char* base = bbase + (size_t)ks * C::TK * a.ldb * 2;
 #pragma unroll
@@ -259,8 +253,8 @@ __global__ __launch_bounds__(C::NTHR, C::MINB) void train_gemm_kernel(GemmArgs a
   auto zero_tail = [&](unsigned char* sa, unsigned char* sb, int left) {
     const uint4 z = make_uint4(0, 0, 0, 0);
     auto kc = [&](unsigned char* p, int rows) {
-      for (int i = threadIdx.x; i < rows * 8; i += C::NTHR)
-        if (((i & 7) ^ kc_swz(i >> 3)) * 8 >= left) reinterpret_cast<uint4*>(p)[i] = z;
+      for (int i = threadIdx.x; i < rows * KCPR; i += C::NTHR)
+        if (((i % KCPR) ^ kc_swz<C::TK>(i / KCPR)) * 8 >= left) reinterpret_cast<uint4*>(p)[i] = z;
     };
     auto mc = [&](unsigned char* p, int cols) {
       for (int i = left * (cols / 8) + threadIdx.x; i < C::TK * (cols / 8); i += C::NTHR)
@@ -290,38 +284,45 @@ __global__ __launch_bounds__(C::NTHR, C::MINB) void train_gemm_kernel(GemmArgs a
 #pragma unroll
   for (int mi = 0; mi < C::MFM; ++mi) {
     const int r = wm * C::WTM + mi * 32;
-    asw[mi] = kc_swz(r + lrow);
-    aoff[mi] = AKC ? (r + lrow) * 128
+    asw[mi] = kc_swz<C::TK>(r + lrow);
+    aoff[mi] = AKC ? (r + lrow) * (C::TK * 2)
                    : trk * (C::TM * 2) + (((r >> 5) ^ (trk & 3)) << 6) + trc;
   }
 #pragma unroll
   for (int ni = 0; ni < C::MFN; ++ni) {
     const int r = nbase[ni];
-    bsw[ni] = kc_swz(r + lrow);
-    boff[ni] = BKC ? (r + lrow) * 128
+    bsw[ni] = kc_swz<C::TK>(r + lrow);
+    boff[ni] = BKC ? (r + lrow) * (C::TK * 2)
                    : trk * (C::TN * 2) + (((r >> 5) ^ (trk & 3)) << 6) + trc;
   }
-  auto tr_frag = [&](const unsigned char* p, int row_bytes) {
-    const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p));
-    const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p + 4 * row_bytes));
-    return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-  };
-  auto load_frags = [&](const unsigned char* sa, const unsigned char* sb, int kk, bf16x8_t* af,
-                        bf16x8_t* bf) {
-    const int c = kk * 2 + khalf;
+  // fragments of step KK (16 along the contraction); KC by ordinary LDS reads,
+  // which the compiler schedules, MC by tr_read
+  auto load_a = [&](const unsigned char* sa, auto kk_c, bf16x8_t (&af)[C::MFM], auto live_c) {
+    constexpr int KK = decltype(kk_c)::value;
+    if constexpr (AKC) {
 #pragma unroll
-    for (int mi = 0; mi < C::MFM; ++mi) {
-      if constexpr (AKC)
-        af[mi] = *reinterpret_cast<const bf16x8_t*>(sa + aoff[mi] + ((c ^ asw[mi]) * 16));
-      else
-        af[mi] = tr_frag(sa + aoff[mi] + kk * 16 * (C::TM * 2), C::TM * 2);
+      for (int mi = 0; mi < decltype(live_c)::value; ++mi)
+        af[mi] = *reinterpret_cast<const bf16x8_t*>(sa + aoff[mi] +
+                                                    (((KK * 2 + khalf) ^ asw[mi]) * 16));
+    } else {
+      uint32_t at[C::MFM];
+#pragma unroll
+      for (int mi = 0; mi < C::MFM; ++mi) at[mi] = lds_addr(sa) + aoff[mi];
+      tr_read<KK * 16 * C::TM * 2, C::TM * 2>(at, af);
     }
+  };
+  auto load_b = [&](const unsigned char* sb, auto kk_c, bf16x8_t (&bf)[C::MFN]) {
+    constexpr int KK = decltype(kk_c)::value;
+    if constexpr (BKC) {
 #pragma unroll
-    for (int ni = 0; ni < C::MFN; ++ni) {
-      if constexpr (BKC)
-        bf[ni] = *reinterpret_cast<const bf16x8_t*>(sb + boff[ni] + ((c ^ bsw[ni]) * 16));
-      else
-        bf[ni] = tr_frag(sb + boff[ni] + kk * 16 * (C::TN * 2), C::TN * 2);
+      for (int ni = 0; ni < C::MFN; ++ni)
+        bf[ni] = *reinterpret_cast<const bf16x8_t*>(sb + boff[ni] +
+                                                    (((KK * 2 + khalf) ^ bsw[ni]) * 16));
+    } else {
+      uint32_t at[C::MFN];
+#pragma unroll
+      for (int ni = 0; ni < C::MFN; ++ni) at[ni] = lds_addr(sb) + boff[ni];
+      tr_read<KK * 16 * C::TN * 2, C::TN * 2>(at, bf);
     }
   };
 
@@ -333,44 +334,74 @@ __global__ __launch_bounds__(C::NTHR, C::MINB) void train_gemm_kernel(GemmArgs a
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
 
-  auto multiply = [&](const unsigned char* sa, const unsigned char* sb) {
-    constexpr int STEPS = C::TK / 16;
-    bf16x8_t af[2][C::MFM], bf[2][C::MFN];
-    load_frags(sa, sb, 0, af[0], bf[0]);
+  // LIVE: the wave's 32-row subtiles that hold rows
+  auto multiply = [&](const unsigned char* sa, const unsigned char* sb, auto live_c) {
+    constexpr int STEPS = C::TK / 16, LIVE = decltype(live_c)::value;
+    if constexpr (LIVE > 0) {
+      bf16x8_t af[2][C::MFM], bf[2][C::MFN];
+      auto load = [&](auto kk_c) {
+        constexpr int KK = decltype(kk_c)::value;
+        load_a(sa, kk_c, af[KK & 1], live_c);
+        load_b(sb, kk_c, bf[KK & 1]);
+      };
+      auto step = [&](auto kk_c) {
+        constexpr int KK = decltype(kk_c)::value, CUR = KK & 1;
+        // KC only: the next step's LDS reads go out ahead of this step's
+        // products; transposed reads wait where they stand
+        constexpr bool AHEAD = AKC && BKC;
+        if constexpr (!AHEAD) load(kk_c);
+        else if constexpr (KK == 0) load(kk_c);
+        if constexpr (AHEAD && KK + 1 < STEPS) load(std::integral_constant<int, KK + 1>{});
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int kk = 0; kk < STEPS; ++kk) {
-      const int cur = kk & 1;
-      if (kk + 1 < STEPS) load_frags(sa, sb, kk + 1, af[cur ^ 1], bf[cur ^ 1]);
-      __builtin_amdgcn_sched_barrier(0);   // the next step's LDS reads stay ahead
+        for (int mi = 0; mi < LIVE; ++mi)
 #pragma unroll
-      for (int mi = 0; mi < C::MFM; ++mi)
-#pragma unroll
-        for (int ni = 0; ni < C::MFN; ++ni)
-          acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf[cur][ni], af[cur][mi],
-                                                                acc[mi][ni], 0, 0, 0);
+          for (int ni = 0; ni < C::MFN; ++ni)
+            acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf[CUR][ni], af[CUR][mi],
+                                                                  acc[mi][ni], 0, 0, 0);
+      };
+      step(std::integral_constant<int, 0>{});
+      step(std::integral_constant<int, 1>{});
+      if constexpr (STEPS > 2) {
+        step(std::integral_constant<int, 2>{});
+        step(std::integral_constant<int, 3>{});
+      }
     }
   };
 
   constexpr int NL = C::ALOADS + C::BLOADS;
   if (nk > 0) {
-    load_tok(0);
 #pragma unroll
     for (int s0 = 0; s0 < C::STAGES - 1; ++s0)
       if (s0 < nk) issue(s0, s0);
   }
-  for (int ks = 0; ks < nk; ++ks) {
-    // chunk ks has landed once at most the younger chunks' loads are
-    // outstanding; past the barrier that holds for every wave, and nobody
-    // still reads the buffer refilled below
-    if (C::STAGES > 2 && ks + 1 < nk) wait_stage_barrier<(C::STAGES - 2) * NL>();
-    else wait_stage_barrier<0>();
-    if (ks + C::STAGES - 1 < nk) issue(ks + C::STAGES - 1, (ks + C::STAGES - 1) % C::STAGES);
-    unsigned char* sa = smem + (ks % C::STAGES) * C::SBYTES;
-    unsigned char* sb = sa + C::ABYTES;
-    const int left = K - ks * C::TK;
-    if (left < C::TK) zero_tail(sa, sb, left);     // (K is a multiple of 8 where KC)
-    multiply(sa, sb);
-  }
+  auto contract = [&](auto live_c) {
+    for (int ks = 0; ks < nk; ++ks) {
+      // chunk ks has landed once at most the younger chunks' loads are
+      // outstanding; past the barrier that holds for every wave, and nobody
+      // still reads the buffer refilled below
+      static_assert(C::STAGES <= 4, "counted waits");
+      const int younger = min(nk - 1 - ks, C::STAGES - 2);
+      if (younger == 2) wait_stage_barrier<(C::STAGES > 3 ? 2 : 0) * NL>();
+      else if (younger == 1) wait_stage_barrier<(C::STAGES > 2 ? 1 : 0) * NL>();
+      else wait_stage_barrier<0>();
+      if (ks + C::STAGES - 1 < nk) issue(ks + C::STAGES - 1, (ks + C::STAGES - 1) % C::STAGES);
+      unsigned char* sa = smem + (ks % C::STAGES) * C::SBYTES;
+      unsigned char* sb = sa + C::ABYTES;
+      const int left = K - ks * C::TK;
+      if (left < C::TK) zero_tail(sa, sb, left);     // (K is a multiple of 8 where KC)
+      multiply(sa, sb, live_c);
+    }
+  };
+  // An expert's last tile may hold few rows: a wave without rows only loads,
+  // and one with at most half its subtiles skips the products of the others.
+  // (Each case is a loop of its own, chosen once per wave.)
+  const int live = r1 - r0 - wm * C::WTM;      // rows of this wave's part
+  constexpr int HALF_M = (C::MFM + 1) / 2;
+  if (WGRAD || live > 32 * HALF_M) contract(std::integral_constant<int, C::MFM>{});
+  else if (live > 32) contract(std::integral_constant<int, HALF_M>{});
+  else if (live > 0) contract(std::integral_constant<int, 1>{});
+  else contract(std::integral_constant<int, 0>{});
 
   // ---- epilogue: output tiles leave through LDS, whole lines at a time.
   // acc[mi][ni][4 q + r] is row m0 + lrow, column nbase + 8 q + 4 khalf + r.
@@ -441,12 +472,18 @@ __global__ __launch_bounds__(C::NTHR, C::MINB) void train_gemm_kernel(GemmArgs a
   }
   if constexpr (EPI == EPI_DSWIGLU) {
     // dg, du and h of each element from dh (the accumulator, never rounded)
-    // and the saved g and u; dg and du share the accumulator's register
-    uint32_t hp[C::MFM][C::MFN][8];
+    // and the saved g and u, 32 rows of every wave at a time: the three
+    // results of those rows fill LDS side by side and leave together (h after
+    // the others where LDS holds two)
+    constexpr int RB = C::WM * 32, REGION = RB * C::PITCH;
+    constexpr bool THREE = 3 * REGION <= C::LDS;
+    static_assert(2 * REGION <= C::LDS, "staged rows");
 #pragma unroll
     for (int mi = 0; mi < C::MFM; ++mi) {
       const int row = min(r0 + wm * C::WTM + mi * 32 + lrow, r1 - 1);
       const float* gr = a.gu + (size_t)row * (2 * (size_t)a.N);
+      unsigned char* so = smem + (wm * 32 + lrow) * C::PITCH;
+      uint2 hp[C::MFN][4];
 #pragma unroll
       for (int ni = 0; ni < C::MFN; ++ni) {
         const int col = n0 + nbase[ni] < a.N ? n0 + nbase[ni] : 0;   // whole 32s in or out
@@ -456,55 +493,141 @@ __global__ __launch_bounds__(C::NTHR, C::MINB) void train_gemm_kernel(GemmArgs a
           const float4 g4 = *reinterpret_cast<const float4*>(gr + c);
           const float4 u4 = *reinterpret_cast<const float4*>(gr + a.N + c);
           const float g[4] = {g4.x, g4.y, g4.z, g4.w}, u[4] = {u4.x, u4.y, u4.z, u4.w};
-          float h[4];
+          float dg[4], du[4], h[4];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const float dh = acc[mi][ni][4 * q + r];
-            const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-g[r]));
-            const float sg = g[r] * s;
+            const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-g[r])), sg = g[r] * s;
             h[r] = sg * u[r];
-            const uint32_t p = cvt_bf16x2(dh * u[r] * (s + sg * (1.0f - s)), dh * sg);
-            acc[mi][ni][4 * q + r] = __uint_as_float(p);
+            dg[r] = dh * u[r] * (s + sg * (1.0f - s));
+            du[r] = dh * sg;
           }
-          hp[mi][ni][2 * q] = cvt_bf16x2(h[0], h[1]);
-          hp[mi][ni][2 * q + 1] = cvt_bf16x2(h[2], h[3]);
+          uint2* p = reinterpret_cast<uint2*>(so + (nbase[ni] + 8 * q + 4 * khalf) * 2);
+          p[0] = make_uint2(cvt_bf16x2(dg[0], dg[1]), cvt_bf16x2(dg[2], dg[3]));
+          p[REGION / 8] = make_uint2(cvt_bf16x2(du[0], du[1]), cvt_bf16x2(du[2], du[3]));
+          hp[ni][q] = make_uint2(cvt_bf16x2(h[0], h[1]), cvt_bf16x2(h[2], h[3]));
+          if (THREE) p[2 * REGION / 8] = hp[ni][q];
         }
-        // g and u of one subtile at a time: all of them at once would spill
-        __builtin_amdgcn_sched_barrier(0);
       }
-    }
-    auto pass = [&](int which) {
-#pragma unroll
-      for (int mi = 0; mi < C::MFM; ++mi)
+      auto leave = [&](bf16_t* y, long long ld, int region) {
+        constexpr int CPR = C::TN / 8;
+        for (int c = threadIdx.x; c < RB * CPR; c += C::NTHR) {
+          const int r = c / CPR, cc = c - r * CPR, col = n0 + cc * 8;
+          const int rt = (r >> 5) * C::WTM + mi * 32 + (r & 31);     // row of the tile
+          if (rt < nrows && col < a.N)
+            st_nt16(y + (size_t)(r0 + rt) * ld + col,
+                    *reinterpret_cast<const uint4*>(smem + region + r * C::PITCH + cc * 16));
+        }
+      };
+      lds_barrier();
+      leave(out, a.ldo, 0);
+      leave(out + a.up_off, a.ldo, REGION);
+      if constexpr (!THREE) {
+        lds_barrier();
 #pragma unroll
         for (int ni = 0; ni < C::MFN; ++ni)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t p[4];
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<uint2*>(so + (nbase[ni] + 8 * q + 4 * khalf) * 2) = hp[ni][q];
+        lds_barrier();
+      }
+      leave(a.out2, a.N, THREE ? 2 * REGION : 0);
+      lds_barrier();
+    }
+  }
+}
+
+// Row tiles of an expert: 256 rows while it has them; the last tile, if it
+// holds at most 128 or 64, in a shape of its own whose shorter stages leave LDS
+// for three and four of them.  (Few rows leave nothing to hide a load's
+// latency behind but other loads: with two stages a last tile of 6 rows took as
+// long as a full one.)  At least 64 rows' worth of weights per block either way.
+using GemmT256 = GemmCfg<256, 256, 64, 2, 2, 4>;
+using GemmT128 = GemmCfg<128, 256, 64, 3, 2, 4>;
+using GemmT64 = GemmCfg<64, 256, 64, 4, 2, 4>;
+constexpr int GEMM_TM = GemmT256::TM, GEMM_TN = GemmT256::TN;
+constexpr int GEMM_LDS = std::max({GemmT256::LDS, GemmT128::LDS, GemmT64::LDS});
+
+template <bool BKC, int EPI, bool GATHER>
+__global__ __launch_bounds__(512, 2) void train_rows_kernel(GemmArgs a) {
+  extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
+  constexpr int COLS = EPI == EPI_SWIGLU ? GEMM_TN / 2 : GEMM_TN;
+  const int NT = (a.N + COLS - 1) / COLS;
+  TileScan scan;
+  scan.init(a.offsets, a.E, GEMM_TM, a.max_rows);
+  int b = blockIdx.x;
+  const int n_active = scan.total * NT, per = n_active >> 3;
+  if (b >= n_active) return;
+  if (b < per * 8) b = (b & 7) * per + (b >> 3);       // contiguous numbers share an XCD's L2
+  const RowTile t = scan.find(a.offsets, a.E, GEMM_TM, a.max_rows, b / NT);
+  // An expert's tiles of 129 rows and more first, then its short last tile: a
+  // CU left with a short one at the end waits less.  Within them, the 32 blocks
+  // of an XCD take all row tiles of a column while they are few, else 4 columns
+  // side by side (one column of 32 row tiles ran 10-25% slower).
+  const int rows = t.end - t.off, te = (rows + GEMM_TM - 1) / GEMM_TM;
+  const int li = b - t.first * NT, last = rows - (te - 1) * GEMM_TM;
+  const int tall = last > 128 ? te : te - 1;
+  int m_t = te - 1, n_t = li - tall * NT;
+  if (n_t < 0) {
+    const int group = tall > 8 ? 4 : 1;
+    const int g = li / (tall * group), rem = li - g * tall * group, Gc = min(group, NT - g * group);
+    m_t = rem / Gc;
+    n_t = g * group + (rem - m_t * Gc);
+  }
+  const int n0 = n_t * COLS;
+  const int r0 = t.off + m_t * GEMM_TM, r1 = min(r0 + GEMM_TM, t.end);
+  if (r1 - r0 > 128) gemm_tile<GemmT256, false, BKC, EPI, GATHER>(a, smem, t.e, r0, r1, n0, a.K, 0);
+  else if (r1 - r0 > 64) gemm_tile<GemmT128, false, BKC, EPI, GATHER>(a, smem, t.e, r0, r1, n0, a.K, 0);
+  else gemm_tile<GemmT64, false, BKC, EPI, GATHER>(a, smem, t.e, r0, r1, n0, a.K, 0);
+}
+
+// Weight gradients: contractions as long as an expert has rows, often a few
+// hundred, so a block's start and its output are a good part of its time:
+// chunks of 32 rows and 128 x 256 outputs leave room for two blocks per CU, one
+// computing while the other stores (Mixtral shape, 1024 rows per expert: dW2
+// 1.04 -> 0.95 ms; 32 rows per expert: 0.43 -> 0.30 ms, 5.3 TB/s of stores).
+using GemmW = GemmCfg<128, 256, 32, 2, 2, 4>;
+
+__global__ __launch_bounds__(512, 4) void train_wgrad_kernel(GemmArgs a) {
+  extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
+  constexpr int GROUP = 8;      // column tiles side by side
+  const int NT = (a.N + GemmW::TN - 1) / GemmW::TN, MT = (a.M + GemmW::TM - 1) / GemmW::TM;
+  const int n_active = a.E * MT * NT, per = n_active >> 3;
+  int b = blockIdx.x;
+  if (b < per * 8) b = (b & 7) * per + (b >> 3);
+  const int e = b / (MT * NT), li = b - e * MT * NT;
+  const int g = li / (MT * GROUP), rem = li - g * MT * GROUP, Gc = min(GROUP, NT - g * GROUP);
+  const int m_t = rem / Gc, n0 = (g * GROUP + (rem - m_t * Gc)) * GemmW::TN;
+  const int r0 = m_t * GemmW::TM, r1 = min(r0 + GemmW::TM, a.M);
+  const int o = a.offsets[e], K = expert_tiles(o, a.offsets[e + 1], 1, a.max_rows);
+  gemm_tile<GemmW, true, false, EPI_STORE, false>(a, smem, e, r0, r1, n0, K, K ? o : 0);
+}
+
+// ---------------------------------------------------------------------------
+// a_perm[r] = x[src_token[r]] for the rows of valid experts: dW13 reads its rows
+// in order (with the gather inside the product's loads it ran 15-20% slower at
+// 512-1024 rows per expert, more than the copy costs).  A wave per row.
+// ---------------------------------------------------------------------------
+constexpr int GR_ROWS = 16;      // rows per block of 4 waves
+
+__global__ __launch_bounds__(256) void train_gather_kernel(const uint4* x, const int32_t* src_token,
+                                                           const int32_t* offsets, int E,
+                                                           int max_rows, int vecs, uint4* out) {
+  const int lane = threadIdx.x & 63;
+  const int row0 = blockIdx.x * GR_ROWS + (threadIdx.x >> 6) * (GR_ROWS / 4);
+  bool mine[GR_ROWS / 4] = {};
+  for (int e = lane; e < E; e += 64) {
+    const int o = offsets[e], end = offsets[e + 1];
+    if (expert_tiles(o, end, 1, max_rows) == 0) continue;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) p[r] = __float_as_uint(acc[mi][ni][4 * q + r]);
-            const uint32_t sel = which ? 0x07060302u : 0x05040100u;   // high halves, or low
-            put(mi, nbase[ni] + 8 * q + 4 * khalf, __builtin_amdgcn_perm(p[1], p[0], sel),
-                __builtin_amdgcn_perm(p[3], p[2], sel));
-          }
-    };
-    pass(0);
-    lds_barrier();
-    store(out, a.ldo);
-    lds_barrier();
-    pass(1);
-    lds_barrier();
-    store(out + a.up_off, a.ldo);
-    lds_barrier();
+    for (int i = 0; i < GR_ROWS / 4; ++i) mine[i] |= row0 + i >= o && row0 + i < end;
+  }
 #pragma unroll
-    for (int mi = 0; mi < C::MFM; ++mi)
-#pragma unroll
-      for (int ni = 0; ni < C::MFN; ++ni)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          put(mi, nbase[ni] + 8 * q + 4 * khalf, hp[mi][ni][2 * q], hp[mi][ni][2 * q + 1]);
-    lds_barrier();
-    store(a.out2, a.N);
+  for (int i = 0; i < GR_ROWS / 4; ++i) {
+    if (__ballot(mine[i]) == 0) continue;
+    const size_t row = row0 + i;
+    const uint4* s = x + (size_t)max(src_token[row], 0) * vecs;
+    for (int c = lane; c < vecs; c += 64) out[row * vecs + c] = s[c];
   }
 }
 
@@ -574,8 +697,7 @@ __global__ __launch_bounds__(256) void train_f32_kernel(F32GemmArgs a) {
           vb = B[(size_t)(n0 + bn) * a.ldb + k0 + bk];
           if (EPI == EPI_SWIGLU) vu = B[(size_t)(a.up_off + n0 + bn) * a.ldb + k0 + bk];
         } else if constexpr (WGRAD) {
-          const int kr = krow0 + k0 + bk, row = a.src_token ? max(a.src_token[kr], 0) : kr;
-          vb = B[(size_t)row * a.ldb + n0 + bn];
+          vb = B[(size_t)(krow0 + k0 + bk) * a.ldb + n0 + bn];
         } else {
           vb = B[(size_t)(k0 + bk) * a.ldb + n0 + bn];
         }
@@ -625,41 +747,46 @@ __global__ __launch_bounds__(256) void train_f32_kernel(F32GemmArgs a) {
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-using GemmBig = GemmCfg<256, 256, 2, 2, 4, 1>;
-using GemmMed = GemmCfg<128, 256, 3, 2, 4, 1>;
-
 static long long row_tiles(int max_rows, int E, int BM) {
   const long long bound = ((long long)max_rows + (long long)E * (BM - 1)) / BM;
   return bound < max_rows ? bound : max_rows;
 }
 static long long cdivl(long long a, long long b) { return (a + b - 1) / b; }
 
-template <class C, bool WGRAD, bool BKC, int EPI, bool GATHER>
-static hipError_t launch_gemm_t(const GemmArgs& a, hipStream_t st) {
+template <bool BKC, int EPI, bool GATHER>
+static hipError_t launch_rows(const GemmArgs& a, hipStream_t st) {
   static std::atomic<uint64_t> lds_set{0};
   hipError_t err = ensure_lds_limit(
-      reinterpret_cast<const void*>(&train_gemm_kernel<C, WGRAD, BKC, EPI, GATHER>), C::LDS, lds_set);
+      reinterpret_cast<const void*>(&train_rows_kernel<BKC, EPI, GATHER>), GEMM_LDS, lds_set);
   if (err != hipSuccess) return err;
-  constexpr int cols = EPI == EPI_SWIGLU ? C::TN / 2 : C::TN;
-  const long long nt = cdivl(a.N, cols);
-  const long long grid = (WGRAD ? a.E * cdivl(a.M, C::TM) : row_tiles(a.max_rows, a.E, C::TM)) * nt;
+  const long long nt = cdivl(a.N, EPI == EPI_SWIGLU ? GEMM_TN / 2 : GEMM_TN);
+  const long long grid = row_tiles(a.max_rows, a.E, GEMM_TM) * nt;
   if (grid <= 0) return hipSuccess;
   if (grid > INT32_MAX) return hipErrorInvalidValue;
-  train_gemm_kernel<C, WGRAD, BKC, EPI, GATHER><<<(unsigned)grid, C::NTHR, C::LDS, st>>>(a);
+  train_rows_kernel<BKC, EPI, GATHER><<<(unsigned)grid, 512, GEMM_LDS, st>>>(a);
+  return hipGetLastError();
+}
+
+static hipError_t launch_wgrad(const GemmArgs& a, hipStream_t st) {
+  static std::atomic<uint64_t> lds_set{0};
+  hipError_t err = ensure_lds_limit(reinterpret_cast<const void*>(&train_wgrad_kernel), GemmW::LDS,
+                                    lds_set);
+  if (err != hipSuccess) return err;
+  const long long grid = a.E * cdivl(a.M, GemmW::TM) * cdivl(a.N, GemmW::TN);
+  if (grid > INT32_MAX) return hipErrorInvalidValue;
+  train_wgrad_kernel<<<(unsigned)grid, 512, GemmW::LDS, st>>>(a);
   return hipGetLastError();
 }
 
 template <bool WGRAD, bool BKC, int EPI>
 static hipError_t launch_gemm(const GemmArgs& a, hipStream_t st) {
-  const int mean = (int)cdivl(a.max_rows, a.E);
-  const bool big = WGRAD ? true : mean >= 384;
-  if constexpr (EPI == EPI_SWIGLU || WGRAD) {
-    if (a.src_token)
-      return big ? launch_gemm_t<GemmBig, WGRAD, BKC, EPI, true>(a, st)
-                 : launch_gemm_t<GemmMed, WGRAD, BKC, EPI, true>(a, st);
+  if constexpr (WGRAD) {
+    return launch_wgrad(a, st);
+  } else {
+    if constexpr (EPI == EPI_SWIGLU)
+      if (a.src_token) return launch_rows<BKC, EPI, true>(a, st);
+    return launch_rows<BKC, EPI, false>(a, st);
   }
-  return big ? launch_gemm_t<GemmBig, WGRAD, BKC, EPI, false>(a, st)
-             : launch_gemm_t<GemmMed, WGRAD, BKC, EPI, false>(a, st);
 }
 
 template <bool WGRAD, bool BKC, int EPI>
@@ -687,7 +814,7 @@ static hipError_t product(const TrainFfn& f, const void* A, long long lda, const
   }
   const GemmArgs a{(const bf16_t*)A, (const bf16_t*)B, lda, ldb, b_stride, src, f.offsets, f.E,
                    f.max_rows, M, N, K, up_off, (bf16_t*)out, ldo, out_stride, (bf16_t*)out2,
-                   f.gu, WGRAD ? 4 : 1};
+                   f.gu};
   return launch_gemm<WGRAD, BKC, EPI>(a, st);
 }
 
@@ -701,8 +828,8 @@ hipError_t launch_train_forward(const TrainFfn& f, void* y, hipStream_t st) {
                                          nullptr, st);
 }
 
-hipError_t launch_train_backward(const TrainFfn& f, const void* dy, void* dgu, void* dx, void* dw13,
-                                 void* dw2, hipStream_t st) {
+hipError_t launch_train_backward(const TrainFfn& f, const void* dy, void* dgu, void* x_perm,
+                                 void* dx, void* dw13, void* dw2, hipStream_t st) {
   const long long H = f.H, I = f.I;
   hipError_t err = product<false, false, EPI_DSWIGLU>(f, dy, H, f.w2, I, H * I, false, 0, f.I, f.H,
                                                       f.I, dgu, 2 * I, 0, f.h, st);
@@ -716,7 +843,15 @@ hipError_t launch_train_backward(const TrainFfn& f, const void* dy, void* dgu, v
   err = product<true, false, EPI_STORE>(f, dy, H, f.h, I, 0, false, f.H, f.I, 0, 0, dw2, I, H * I,
                                         nullptr, st);
   if (err != hipSuccess) return err;
-  return product<true, false, EPI_STORE>(f, dgu, 2 * I, f.x, H, 0, true, 2 * f.I, f.H, 0, 0, dw13, H,
+  const void* a = f.x;
+  if (f.src_token) {
+    train_gather_kernel<<<(unsigned)cdivl(f.max_rows, GR_ROWS), 256, 0, st>>>(
+        static_cast<const uint4*>(f.x), f.src_token, f.offsets, f.E, f.max_rows,
+        f.H * (f.dt == 0 ? 4 : 2) / 16, static_cast<uint4*>(x_perm));
+    if ((err = hipGetLastError()) != hipSuccess) return err;
+    a = x_perm;
+  }
+  return product<true, false, EPI_STORE>(f, dgu, 2 * I, a, H, 0, false, 2 * f.I, f.H, 0, 0, dw13, H,
                                          2 * I * H, nullptr, st);
 }
 

@@ -41,9 +41,10 @@ struct TrainFfn {
 constexpr int OPS_MAX_DIM = 65536;               // H and I of the expert blocks
 constexpr long long OPS_MAX_HI = 1ll << 30;      // H * I: an expert's weights within 4 GiB
 hipError_t launch_train_forward(const TrainFfn& f, void* y, hipStream_t st);
-// dgu: [max_rows][2 I], workspace; dx, or dw13 with dw2, may be null
-hipError_t launch_train_backward(const TrainFfn& f, const void* dy, void* dgu, void* dx, void* dw13,
-                                 void* dw2, hipStream_t st);
+// dgu: [max_rows][2 I], workspace; x_perm: [max_rows][H], workspace of the
+// gathered form; dx, or dw13 with dw2, may be null
+hipError_t launch_train_backward(const TrainFfn& f, const void* dy, void* dgu, void* x_perm,
+                                 void* dx, void* dw13, void* dw2, hipStream_t st);
 
 // ffn_mxfp8.hip: the grouped SwiGLU experts on MXFP8 rows and weights.
 struct MxFfn {

@@ -116,8 +116,8 @@ int moe_grouped_ffn_train(const void* x_perm, const void* x, const int32_t* src_
 
 size_t moe_grouped_ffn_backward_workspace_size(int max_rows, int E_loc, int H, int I_loc, int dt) {
   if (!valid_dt(dt) || check_block(max_rows, E_loc, H, I_loc) != MOE_OK) return 0;
-  const size_t row = (size_t)I_loc * elt_bytes(dt), rows = max_rows > 0 ? max_rows : 1;
-  return align_up(rows * row) + align_up(rows * row * 2);
+  const size_t eb = elt_bytes(dt), rows = max_rows > 0 ? max_rows : 1;
+  return align_up(rows * I_loc * eb) + align_up(rows * I_loc * eb * 2) + align_up(rows * H * eb);
 }
 
 int moe_grouped_ffn_backward(const void* dy_perm, const void* x_perm, const void* x,
@@ -146,9 +146,10 @@ int moe_grouped_ffn_backward(const void* dy_perm, const void* x_perm, const void
   Carver c(ws);
   void* h = c.take<char>((size_t)max_rows * I_loc * elt_bytes(dt));
   void* dgu = c.take<char>((size_t)max_rows * I_loc * elt_bytes(dt) * 2);
+  void* xp = c.take<char>((size_t)max_rows * H * elt_bytes(dt));
   const TrainFfn f{x_perm ? x_perm : x, x_perm ? nullptr : src_token, offsets, E_loc, max_rows, H,
                    I_loc, dt, w13, w2, const_cast<float*>(gu), h};
-  return hip_status(launch_train_backward(f, dy_perm, dgu, dx_perm, dw13, dw2, s));
+  return hip_status(launch_train_backward(f, dy_perm, dgu, xp, dx_perm, dw13, dw2, s));
 }
 
 size_t moe_grouped_ffn_mxfp8_workspace_size(int max_rows, int E_loc, int H, int I_loc) {
