@@ -588,12 +588,15 @@ __global__ __launch_bounds__(512, 2) void train_rows_kernel(GemmArgs a) {
 // 1.04 -> 0.95 ms; 32 rows per expert: 0.43 -> 0.30 ms, 5.3 TB/s of stores).
 using GemmW = GemmCfg<128, 256, 32, 2, 2, 4>;
 
-__global__ __launch_bounds__(512, 4) void train_wgrad_kernel(GemmArgs a) {
+// One launch for both parameters: blocks [0, grid0) take a0, the rest a1.
+__global__ __launch_bounds__(512, 4) void train_wgrad_kernel(GemmArgs a0, GemmArgs a1, int grid0) {
+  const bool second = (int)blockIdx.x >= grid0;
+  const GemmArgs a = second ? a1 : a0;
   extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
   constexpr int GROUP = 8;      // column tiles side by side
   const int NT = (a.N + GemmW::TN - 1) / GemmW::TN, MT = (a.M + GemmW::TM - 1) / GemmW::TM;
   const int n_active = a.E * MT * NT, per = n_active >> 3;
-  int b = blockIdx.x;
+  int b = second ? (int)blockIdx.x - grid0 : (int)blockIdx.x;
   if (b < per * 8) b = (b & 7) * per + (b >> 3);
   const int e = b / (MT * NT), li = b - e * MT * NT;
   const int g = li / (MT * GROUP), rem = li - g * MT * GROUP, Gc = min(GROUP, NT - g * GROUP);
@@ -632,8 +635,13 @@ __global__ __launch_bounds__(256) void train_gather_kernel(const uint4* x, const
 }
 
 // ---------------------------------------------------------------------------
-// float32: the same products on 64 x 64 tiles by plain multiply-adds (the
-// float32 layer is small).
+// float32: the same products by v_mfma_f32_16x16x4_f32 straight from memory.
+// The float32 layer is small (the toy layer has 16 rows per expert), so a
+// block takes 32 x 32 outputs and its 4 waves split the contraction in
+// interleaved chunks of 16, each with the next chunk's loads in flight; they
+// meet in LDS in wave order.  A lane's four elements of a chunk feed four
+// products: element i of lane l stands for k = 4 (l / 16) + i in both operands.
+// (64 x 64 tiles of plain multiply-adds: 343 us for the toy layer's step.)
 // ---------------------------------------------------------------------------
 struct F32GemmArgs {
   const float* A;
@@ -648,26 +656,29 @@ struct F32GemmArgs {
   const float* gu;
 };
 
+constexpr int F32_T = 32;
+
 template <bool WGRAD, bool BKC, int EPI>
-__global__ __launch_bounds__(256) void train_f32_kernel(F32GemmArgs a) {
-  constexpr int T = 64, TK = 16;
-  __shared__ float sa[TK][T + 1], sb[TK][T + 1], su[EPI == EPI_SWIGLU ? TK : 1][T + 1];
-  const int tid = threadIdx.x;
-  const int NT = (a.N + T - 1) / T;
+__device__ __forceinline__ void f32_tile(const F32GemmArgs& a, int block) {
+  constexpr int T = F32_T, NB = EPI == EPI_SWIGLU ? 4 : 2;    // 16-column operands (gate, then up)
+  constexpr int PITCH = NB * 16 + 4;
+  __shared__ __attribute__((aligned(16))) float red[4][T][PITCH];
+  const int lane = threadIdx.x & 63;
+  const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int NT = a.N / T, n0 = (block % NT) * T;
   int e, r0, r1, K, krow0 = 0;
-  const int n0 = (blockIdx.x % NT) * T;
   if constexpr (WGRAD) {
-    const int MT = (a.M + T - 1) / T, li = blockIdx.x / NT;
+    const int MT = a.M / T, li = block / NT;
     e = li / MT;
     r0 = (li - e * MT) * T;
-    r1 = min(r0 + T, a.M);
-    const int o = a.offsets[e], end = a.offsets[e + 1];
-    K = expert_tiles(o, end, 1, a.max_rows);
+    r1 = r0 + T;
+    const int o = a.offsets[e];
+    K = expert_tiles(o, a.offsets[e + 1], 1, a.max_rows);
     krow0 = K ? o : 0;
   } else {
     TileScan scan;
     scan.init(a.offsets, a.E, T, a.max_rows);
-    const int tile = blockIdx.x / NT;
+    const int tile = block / NT;
     if (tile >= scan.total) return;
     const RowTile t = scan.find(a.offsets, a.E, T, a.max_rows, tile);
     e = t.e;
@@ -675,73 +686,125 @@ __global__ __launch_bounds__(256) void train_f32_kernel(F32GemmArgs a) {
     r1 = min(r0 + T, t.end);
     K = a.K;
   }
-  const float* B = WGRAD ? a.B : a.B + (size_t)e * a.b_stride;
-  float acc[4][4] = {}, acu[4][4] = {};
-  const int tm = tid >> 4, tn = tid & 15;       // rows tm + 16 i, columns tn + 16 j
-  for (int k0 = 0; k0 < K; k0 += TK) {
-    for (int i = tid; i < TK * T; i += 256) {
-      // consecutive threads along the operand's contiguous direction
-      const int ak = WGRAD ? i / T : i % TK, am = WGRAD ? i % T : i / TK;
-      const int bk = BKC ? i % TK : i / T, bn = BKC ? i / TK : i % T;
-      float va = 0.f, vb = 0.f, vu = 0.f;
-      if (k0 + ak < K && r0 + am < r1) {
-        if constexpr (WGRAD) {
-          va = a.A[(size_t)(krow0 + k0 + ak) * a.lda + r0 + am];
-        } else {
-          const int row = a.src_token ? max(a.src_token[r0 + am], 0) : r0 + am;
-          va = a.A[(size_t)row * a.lda + k0 + ak];
-        }
-      }
-      if (k0 + bk < K && n0 + bn < a.N) {
-        if constexpr (BKC) {
-          vb = B[(size_t)(n0 + bn) * a.ldb + k0 + bk];
-          if (EPI == EPI_SWIGLU) vu = B[(size_t)(a.up_off + n0 + bn) * a.ldb + k0 + bk];
-        } else if constexpr (WGRAD) {
-          vb = B[(size_t)(krow0 + k0 + bk) * a.ldb + n0 + bn];
-        } else {
-          vb = B[(size_t)(k0 + bk) * a.ldb + n0 + bn];
-        }
-      }
-      sa[ak][am] = va;
-      sb[bk][bn] = vb;
-      if (EPI == EPI_SWIGLU) su[EPI == EPI_SWIGLU ? bk : 0][bn] = vu;
+  const int lr = lane & 15, lg = lane >> 4;
+  // (a weight gradient's gathered B starts at row 0: its rows are looked up)
+  const float* B = !WGRAD            ? a.B + (size_t)e * a.b_stride
+                   : a.src_token ? a.B
+                                 : a.B + (size_t)krow0 * a.ldb;
+  const float* ap[2];
+  const float* bp[NB];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if constexpr (WGRAD) {
+      ap[i] = a.A + (size_t)krow0 * a.lda + r0 + 16 * i + lr;
+    } else {
+      const int row = min(r0 + 16 * i + lr, r1 - 1);
+      ap[i] = a.A + (size_t)(a.src_token ? max(a.src_token[row], 0) : row) * a.lda;
     }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < TK; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          acc[i][j] = fmaf(sa[k][tm + 16 * i], sb[k][tn + 16 * j], acc[i][j]);
-          if (EPI == EPI_SWIGLU)
-            acu[i][j] = fmaf(sa[k][tm + 16 * i], su[EPI == EPI_SWIGLU ? k : 0][tn + 16 * j],
-                             acu[i][j]);
-        }
-    __syncthreads();
   }
-  float* out = WGRAD ? a.out + (size_t)e * a.out_stride : a.out;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < NB; ++i) {
+    const int n = n0 + (i & 1) * 16 + lr + (i >> 1) * a.up_off;
+    bp[i] = BKC ? B + (size_t)n * a.ldb : B + n;
+  }
+  // elements k + [0, 4) of a row, or of a column (zeros past the end: only a
+  // weight gradient's contraction ends inside a chunk)
+  auto along = [&](const float* p, int k) {
+    const float4 v = *reinterpret_cast<const float4*>(p + k);
+    return f32x4_t{v.x, v.y, v.z, v.w};
+  };
+  auto across = [&](const float* p, long long ld, int k, const int32_t* src) {
+    f32x4_t v;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int row = r0 + tm + 16 * i, col = n0 + tn + 16 * j;
-      if (row >= r1 || col >= a.N) continue;
-      float* o = out + (size_t)row * a.ldo + col;
-      if constexpr (EPI == EPI_STORE) {
-        *o = acc[i][j];
-      } else if constexpr (EPI == EPI_SWIGLU) {
-        o[0] = acc[i][j];
-        o[a.up_off] = acu[i][j];
-        a.out2[(size_t)row * a.N + col] = silu(acc[i][j]) * acu[i][j];
-      } else {
-        const float* gr = a.gu + (size_t)row * (2 * (size_t)a.N) + col;
-        const float g = gr[0], u = gr[a.N], s = 1.0f / (1.0f + expf(-g)), sg = g * s;
-        o[0] = acc[i][j] * u * (s + sg * (1.0f - s));
-        o[a.up_off] = acc[i][j] * sg;
-        a.out2[(size_t)row * a.N + col] = sg * u;
-      }
+    for (int i = 0; i < 4; ++i) {
+      v[i] = 0.f;
+      if (!WGRAD || k + i < K)
+        v[i] = p[(size_t)(src ? max(src[krow0 + k + i], 0) : k + i) * ld];
     }
+    return v;
+  };
+  struct Chunk16 {
+    f32x4_t a[2], b[NB];
+  };
+  auto load = [&](Chunk16& c, int s) {
+    const int k = s * 16 + 4 * lg;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) c.a[i] = WGRAD ? across(ap[i], a.lda, k, nullptr) : along(ap[i], k);
+#pragma unroll
+    for (int i = 0; i < NB; ++i) c.b[i] = BKC ? along(bp[i], k) : across(bp[i], a.ldb, k, WGRAD ? a.src_token : nullptr);
+  };
+  f32x4_t acc[2][NB];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  auto multiply = [&](const Chunk16& c) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(c.b[j][q], c.a[i][q], acc[i][j], 0, 0, 0);
+  };
+  const int steps = (K + 15) / 16;
+  Chunk16 c0, c1;
+  int s = wid;
+  if (s < steps) load(c0, s);
+  for (; s < steps; s += 8) {
+    if (s + 4 < steps) load(c1, s + 4);
+    multiply(c0);
+    if (s + 4 >= steps) break;
+    if (s + 8 < steps) load(c0, s + 8);
+    multiply(c1);
+  }
+  // lane l holds columns 4 (l / 16) + [0, 4) of row l % 16 of every operand pair
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+      *reinterpret_cast<float4*>(&red[wid][16 * i + lr][16 * j + 4 * lg]) =
+          make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
+  __syncthreads();
+  float* out = WGRAD ? a.out + (size_t)e * a.out_stride : a.out;
+  for (int o = threadIdx.x; o < T * T; o += 256) {
+    const int m = o / T, n = o % T, row = r0 + m, col = n0 + n;
+    if (row >= r1) continue;
+    float v = 0.f, w = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v += red[k][m][n];
+      if (EPI == EPI_SWIGLU) w += red[k][m][EPI == EPI_SWIGLU ? 32 + n : n];
+    }
+    float* p = out + (size_t)row * a.ldo + col;
+    if constexpr (EPI == EPI_STORE) {
+      *p = v;
+    } else if constexpr (EPI == EPI_SWIGLU) {
+      p[0] = v;
+      p[a.up_off] = w;
+      a.out2[(size_t)row * a.N + col] = silu(v) * w;
+    } else {
+      const float* gr = a.gu + (size_t)row * (2 * (size_t)a.N) + col;
+      const float g = gr[0], u = gr[a.N], sig = 1.0f / (1.0f + expf(-g)), sg = g * sig;
+      p[0] = v * u * (sig + sg * (1.0f - sig));
+      p[a.up_off] = v * sg;
+      a.out2[(size_t)row * a.N + col] = sg * u;
+    }
+  }
+}
+
+template <bool BKC, int EPI>
+__global__ __launch_bounds__(256) void train_f32_kernel(F32GemmArgs a) {
+  f32_tile<false, BKC, EPI>(a, blockIdx.x);
+}
+// dx, dW13 and dW2, which need dh's results but not one another's, in one
+// launch: blocks from 0, from b13 and from b2 on.
+__global__ __launch_bounds__(256) void train_f32_grads_kernel(F32GemmArgs ax, F32GemmArgs a13,
+                                                              F32GemmArgs a2, int b13, int b2) {
+  const int b = blockIdx.x;
+  if (b < b13) f32_tile<false, false, EPI_STORE>(ax, b);
+  else if (b < b2) f32_tile<true, false, EPI_STORE>(a13, b - b13);
+  else f32_tile<true, false, EPI_STORE>(a2, b - b2);
 }
 
 // ---------------------------------------------------------------------------
@@ -752,6 +815,14 @@ static long long row_tiles(int max_rows, int E, int BM) {
   return bound < max_rows ? bound : max_rows;
 }
 static long long cdivl(long long a, long long b) { return (a + b - 1) / b; }
+
+// (N, M and a weight's contraction are multiples of 32)
+static long long f32_row_blocks(const F32GemmArgs& a) {
+  return row_tiles(a.max_rows, a.E, F32_T) * (a.N / F32_T);
+}
+static long long f32_wgrad_blocks(const F32GemmArgs& a) {
+  return (long long)a.E * (a.M / F32_T) * (a.N / F32_T);
+}
 
 template <bool BKC, int EPI, bool GATHER>
 static hipError_t launch_rows(const GemmArgs& a, hipStream_t st) {
@@ -767,92 +838,98 @@ static hipError_t launch_rows(const GemmArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-static hipError_t launch_wgrad(const GemmArgs& a, hipStream_t st) {
+static long long wgrad_blocks(const GemmArgs& a) {
+  return a.E * cdivl(a.M, GemmW::TM) * cdivl(a.N, GemmW::TN);
+}
+static hipError_t launch_wgrad(const GemmArgs& a, const GemmArgs& b, hipStream_t st) {
   static std::atomic<uint64_t> lds_set{0};
   hipError_t err = ensure_lds_limit(reinterpret_cast<const void*>(&train_wgrad_kernel), GemmW::LDS,
                                     lds_set);
   if (err != hipSuccess) return err;
-  const long long grid = a.E * cdivl(a.M, GemmW::TM) * cdivl(a.N, GemmW::TN);
+  const long long grid0 = wgrad_blocks(a), grid = grid0 + wgrad_blocks(b);
   if (grid > INT32_MAX) return hipErrorInvalidValue;
-  train_wgrad_kernel<<<(unsigned)grid, 512, GemmW::LDS, st>>>(a);
+  train_wgrad_kernel<<<(unsigned)grid, 512, GemmW::LDS, st>>>(a, b, (int)grid0);
   return hipGetLastError();
 }
 
-template <bool WGRAD, bool BKC, int EPI>
-static hipError_t launch_gemm(const GemmArgs& a, hipStream_t st) {
-  if constexpr (WGRAD) {
-    return launch_wgrad(a, st);
-  } else {
-    if constexpr (EPI == EPI_SWIGLU)
-      if (a.src_token) return launch_rows<BKC, EPI, true>(a, st);
-    return launch_rows<BKC, EPI, false>(a, st);
-  }
-}
-
-template <bool WGRAD, bool BKC, int EPI>
+template <bool BKC, int EPI>
 static hipError_t launch_f32(const F32GemmArgs& a, hipStream_t st) {
-  const long long nt = cdivl(a.N, 64);
-  const long long grid = (WGRAD ? a.E * cdivl(a.M, 64) : row_tiles(a.max_rows, a.E, 64)) * nt;
+  const long long grid = f32_row_blocks(a);
   if (grid <= 0) return hipSuccess;
   if (grid > INT32_MAX) return hipErrorInvalidValue;
-  train_f32_kernel<WGRAD, BKC, EPI><<<(unsigned)grid, 256, 0, st>>>(a);
+  train_f32_kernel<BKC, EPI><<<(unsigned)grid, 256, 0, st>>>(a);
   return hipGetLastError();
 }
 
-// One product in either type.
-template <bool WGRAD, bool BKC, int EPI>
-static hipError_t product(const TrainFfn& f, const void* A, long long lda, const void* B,
-                          long long ldb, long long b_stride, bool gather, int M, int N, int K,
-                          int up_off, void* out, long long ldo, long long out_stride, void* out2,
-                          hipStream_t st) {
-  const int32_t* src = gather ? f.src_token : nullptr;
-  if (f.dt == 0) {
-    const F32GemmArgs a{(const float*)A, (const float*)B, lda, ldb, b_stride, src, f.offsets, f.E,
-                        f.max_rows, M, N, K, up_off, (float*)out, ldo, out_stride, (float*)out2,
-                        f.gu};
-    return launch_f32<WGRAD, BKC, EPI>(a, st);
-  }
-  const GemmArgs a{(const bf16_t*)A, (const bf16_t*)B, lda, ldb, b_stride, src, f.offsets, f.E,
-                   f.max_rows, M, N, K, up_off, (bf16_t*)out, ldo, out_stride, (bf16_t*)out2,
-                   f.gu};
-  return launch_gemm<WGRAD, BKC, EPI>(a, st);
+// One product's operands: rows of A against an expert's B (a weight gradient:
+// b_stride 0, M and N its rows and columns).
+struct Product {
+  const void* A;
+  long long lda;
+  const void* B;
+  long long ldb, b_stride;
+  const int32_t* src;
+  int M, N, K, up_off;
+  void* out;
+  long long ldo, out_stride;
+  void* out2;
+};
+static GemmArgs bf16_args(const TrainFfn& f, const Product& p) {
+  return GemmArgs{(const bf16_t*)p.A, (const bf16_t*)p.B, p.lda, p.ldb, p.b_stride, p.src,
+                  f.offsets, f.E, f.max_rows, p.M, p.N, p.K, p.up_off, (bf16_t*)p.out, p.ldo,
+                  p.out_stride, (bf16_t*)p.out2, f.gu};
+}
+static F32GemmArgs f32_args(const TrainFfn& f, const Product& p) {
+  return F32GemmArgs{(const float*)p.A, (const float*)p.B, p.lda, p.ldb, p.b_stride, p.src,
+                     f.offsets, f.E, f.max_rows, p.M, p.N, p.K, p.up_off, (float*)p.out, p.ldo,
+                     p.out_stride, (float*)p.out2, f.gu};
+}
+template <bool BKC, int EPI>
+static hipError_t rows_product(const TrainFfn& f, const Product& p, hipStream_t st) {
+  if (f.dt == 0) return launch_f32<BKC, EPI>(f32_args(f, p), st);
+  if constexpr (EPI == EPI_SWIGLU)
+    if (p.src) return launch_rows<BKC, EPI, true>(bf16_args(f, p), st);
+  return launch_rows<BKC, EPI, false>(bf16_args(f, p), st);
 }
 
 hipError_t launch_train_forward(const TrainFfn& f, void* y, hipStream_t st) {
   const long long H = f.H, I = f.I;
-  hipError_t err = product<false, true, EPI_SWIGLU>(f, f.x, H, f.w13, H, 2 * I * H, true, 0, f.I,
-                                                    f.H, f.I, f.dt == 0 ? f.gu : nullptr, 2 * I, 0,
-                                                    f.h, st);
+  const Product up{f.x, H, f.w13, H, 2 * I * H, f.src_token, 0, f.I, f.H, f.I, f.gu, 2 * I, 0, f.h};
+  const hipError_t err = rows_product<true, EPI_SWIGLU>(f, up, st);
   if (err != hipSuccess) return err;
-  return product<false, true, EPI_STORE>(f, f.h, I, f.w2, I, H * I, false, 0, f.H, f.I, 0, y, H, 0,
-                                         nullptr, st);
+  const Product down{f.h, I, f.w2, I, H * I, nullptr, 0, f.H, f.I, 0, y, H, 0, nullptr};
+  return rows_product<true, EPI_STORE>(f, down, st);
 }
 
 hipError_t launch_train_backward(const TrainFfn& f, const void* dy, void* dgu, void* x_perm,
                                  void* dx, void* dw13, void* dw2, hipStream_t st) {
   const long long H = f.H, I = f.I;
-  hipError_t err = product<false, false, EPI_DSWIGLU>(f, dy, H, f.w2, I, H * I, false, 0, f.I, f.H,
-                                                      f.I, dgu, 2 * I, 0, f.h, st);
+  const Product pdh{dy, H, f.w2, I, H * I, nullptr, 0, f.I, f.H, f.I, dgu, 2 * I, 0, f.h};
+  const Product pdx{dgu, 2 * I, f.w13, H, 2 * I * H, nullptr, 0, f.H, 2 * f.I, 0, dx, H, 0, nullptr};
+  Product p13{dgu, 2 * I, f.x, H, 0, f.src_token, 2 * f.I, f.H, 0, 0, dw13, H, 2 * I * H, nullptr};
+  const Product p2{dy, H, f.h, I, 0, nullptr, f.H, f.I, 0, 0, dw2, I, H * I, nullptr};
+  hipError_t err = rows_product<false, EPI_DSWIGLU>(f, pdh, st);
   if (err != hipSuccess) return err;
-  if (dx) {
-    err = product<false, false, EPI_STORE>(f, dgu, 2 * I, f.w13, H, 2 * I * H, false, 0, f.H,
-                                           2 * f.I, 0, dx, H, 0, nullptr, st);
-    if (err != hipSuccess) return err;
+  if (f.dt == 0) {
+    // the rest in one launch
+    const F32GemmArgs ax = f32_args(f, pdx), a13 = f32_args(f, p13), a2 = f32_args(f, p2);
+    const long long gx = dx ? f32_row_blocks(ax) : 0, g13 = dw13 ? f32_wgrad_blocks(a13) : 0;
+    const long long grid = gx + g13 + (dw2 ? f32_wgrad_blocks(a2) : 0);
+    if (grid > INT32_MAX) return hipErrorInvalidValue;
+    train_f32_grads_kernel<<<(unsigned)grid, 256, 0, st>>>(ax, a13, a2, (int)gx, (int)(gx + g13));
+    return hipGetLastError();
   }
+  if (dx && (err = rows_product<false, EPI_STORE>(f, pdx, st)) != hipSuccess) return err;
   if (!dw2) return hipSuccess;
-  err = product<true, false, EPI_STORE>(f, dy, H, f.h, I, 0, false, f.H, f.I, 0, 0, dw2, I, H * I,
-                                        nullptr, st);
-  if (err != hipSuccess) return err;
-  const void* a = f.x;
   if (f.src_token) {
     train_gather_kernel<<<(unsigned)cdivl(f.max_rows, GR_ROWS), 256, 0, st>>>(
-        static_cast<const uint4*>(f.x), f.src_token, f.offsets, f.E, f.max_rows,
-        f.H * (f.dt == 0 ? 4 : 2) / 16, static_cast<uint4*>(x_perm));
+        static_cast<const uint4*>(f.x), f.src_token, f.offsets, f.E, f.max_rows, f.H / 8,
+        static_cast<uint4*>(x_perm));
     if ((err = hipGetLastError()) != hipSuccess) return err;
-    a = x_perm;
+    p13.B = x_perm;
+    p13.src = nullptr;
   }
-  return product<true, false, EPI_STORE>(f, dgu, 2 * I, a, H, 0, false, 2 * f.I, f.H, 0, 0, dw13, H,
-                                         2 * I * H, nullptr, st);
+  return launch_wgrad(bf16_args(f, p13), bf16_args(f, p2), st);
 }
 
 }  // namespace moe
