@@ -79,26 +79,15 @@ struct MxCfg {
 
 __device__ __forceinline__ int mx_swz(int r) { return (r >> 1) & 7; }
 
+// One output tile: rows [r0, r1) of expert e, columns from n0 on.
 template <class C, bool SWIGLU, bool OUT_BF16, bool GATHER>
-__global__ __launch_bounds__(C::NTHR, 1) void mx_tile_kernel(MxArgs a) {
-  extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
+__device__ __forceinline__ void mx_tile(const MxArgs& a, unsigned char* smem, int e, int r0, int r1,
+                                        int n0) {
   const int lane = threadIdx.x & 63;
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   constexpr int COLS = SWIGLU ? C::TN / 2 : C::TN;
-  const int NT = (a.N + COLS - 1) / COLS;
-  TileScan scan;
-  scan.init(a.offsets, a.E, C::TM, a.max_rows);
-  int b = blockIdx.x;
-  const int n_active = scan.total * NT, per = n_active >> 3;
-  if (b >= n_active) return;
-  if (b < per * 8) b = (b & 7) * per + (b >> 3);       // contiguous numbers share an XCD's L2
-  const RowTile t = scan.find(a.offsets, a.E, C::TM, a.max_rows, b / NT);
-  const int te = (t.end - t.off + C::TM - 1) / C::TM, li = b - t.first * NT;
-  const int n_t = li / te;
-  const int r0 = t.off + (li - n_t * te) * C::TM, r1 = min(r0 + C::TM, t.end);
-  const int n0 = n_t * COLS;
-  const uint8_t* Be = a.B + (size_t)t.e * a.b_rows * a.K;
-  const uint8_t* Bse = a.Bs + (size_t)t.e * a.b_rows * a.pitch;
+  const uint8_t* Be = a.B + (size_t)e * a.b_rows * a.K;
+  const uint8_t* Bse = a.Bs + (size_t)e * a.b_rows * a.pitch;
 
   auto b_row = [&](int rt) {      // weight row of tile row rt; past the end, the last one
     if (SWIGLU) return rt < COLS ? min(n0 + rt, a.N - 1) : a.N + min(n0 + rt - COLS, a.N - 1);
@@ -137,6 +126,8 @@ __global__ __launch_bounds__(C::NTHR, 1) void mx_tile_kernel(MxArgs a) {
     const uint32_t back = ks * C::TK + kchunk * 16 >= a.K ? kchunk * 16 : 0;
 #pragma unroll
     for (int j = 0; j < C::ALOADS; ++j) {
+      // (64 rows per load; counted waits, beyond two stages, need them all)
+      if (C::STAGES == 2 && j > 0 && 64 * j >= r1 - r0) break;
       if constexpr (GATHER)
         __builtin_amdgcn_global_load_lds((gbl_void_t*)(ap[j] + ks * C::TK - back),
                                          (lds_void_t*)(sa + 8192 * j), 16, 0, 0);
@@ -191,42 +182,55 @@ __global__ __launch_bounds__(C::NTHR, 1) void mx_tile_kernel(MxArgs a) {
   for (int s0 = 0; s0 < C::STAGES - 1; ++s0)
     if (s0 < nk) issue(s0, s0);
   constexpr int NL = C::ALOADS + C::BLOADS;    // at least so many per stage and wave
-  for (int ks = 0; ks < nk; ++ks) {
-    if (C::STAGES > 2 && ks + 1 < nk) wait_stage_barrier<(C::STAGES - 2) * NL>();
-    else wait_stage_barrier<0>();
-    if (ks + C::STAGES - 1 < nk) issue(ks + C::STAGES - 1, (ks + C::STAGES - 1) % C::STAGES);
-    unsigned char* sa = smem + (ks % C::STAGES) * C::SBYTES;
-    const unsigned char* sb = sa + C::ABYTES;
-    const int* sc = reinterpret_cast<const int*>(sb + C::BBYTES);
-    const int left = a.K - ks * C::TK;
-    if (left < C::TK) zero_tail(sa, left);
-    // this lane's blocks: byte 0 of the shifted dword in step 0, byte 2 in step 1
-    int as[C::MFM], bs[C::MFN];
+  // LIVE: the wave's 32-row subtiles that hold rows
+  auto contract = [&](auto live_c) {
+    constexpr int LIVE = decltype(live_c)::value;
+    for (int ks = 0; ks < nk; ++ks) {
+      if (C::STAGES > 2 && ks + 1 < nk) wait_stage_barrier<(C::STAGES - 2) * NL>();
+      else wait_stage_barrier<0>();
+      if (ks + C::STAGES - 1 < nk) issue(ks + C::STAGES - 1, (ks + C::STAGES - 1) % C::STAGES);
+      unsigned char* sa = smem + (ks % C::STAGES) * C::SBYTES;
+      const unsigned char* sb = sa + C::ABYTES;
+      const int* sc = reinterpret_cast<const int*>(sb + C::BBYTES);
+      const int left = a.K - ks * C::TK;
+      if (left < C::TK) zero_tail(sa, left);
+      if constexpr (LIVE > 0) {
+        int as[C::MFM], bs[C::MFN];
+        // this lane's blocks: byte 0 of the shifted dword in step 0, byte 2 in step 1
 #pragma unroll
-    for (int mi = 0; mi < C::MFM; ++mi)
-      as[mi] = (int)((uint32_t)mx_valid_scales(sc[wm * C::WTM + mi * 32 + lrow], left >> 5) >>
-                     (8 * khalf));
-#pragma unroll
-    for (int ni = 0; ni < C::MFN; ++ni)
-      bs[ni] = (int)((uint32_t)mx_valid_scales(sc[C::TM + nbase[ni] + lrow], left >> 5) >>
-                     (8 * khalf));
-    auto step = [&](auto step_c) {
-      constexpr int S = decltype(step_c)::value;
-      i32x8_v af[C::MFM], bf[C::MFN];
-#pragma unroll
-      for (int ni = 0; ni < C::MFN; ++ni) bf[ni] = frag(sb, nbase[ni], S);
-#pragma unroll
-      for (int mi = 0; mi < C::MFM; ++mi) af[mi] = frag(sa, wm * C::WTM + mi * 32, S);
-#pragma unroll
-      for (int mi = 0; mi < C::MFM; ++mi)
+        for (int mi = 0; mi < LIVE; ++mi)
+          as[mi] = (int)((uint32_t)mx_valid_scales(sc[wm * C::WTM + mi * 32 + lrow], left >> 5) >>
+                         (8 * khalf));
 #pragma unroll
         for (int ni = 0; ni < C::MFN; ++ni)
-          acc[mi][ni] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-              bf[ni], af[mi], acc[mi][ni], 0, 0, 2 * S, bs[ni], 2 * S, as[mi]);
-    };
-    step(std::integral_constant<int, 0>{});
-    step(std::integral_constant<int, 1>{});
-  }
+          bs[ni] = (int)((uint32_t)mx_valid_scales(sc[C::TM + nbase[ni] + lrow], left >> 5) >>
+                         (8 * khalf));
+        auto step = [&](auto step_c) {
+          constexpr int S = decltype(step_c)::value;
+          i32x8_v af[C::MFM], bf[C::MFN];
+#pragma unroll
+          for (int ni = 0; ni < C::MFN; ++ni) bf[ni] = frag(sb, nbase[ni], S);
+#pragma unroll
+          for (int mi = 0; mi < LIVE; ++mi) af[mi] = frag(sa, wm * C::WTM + mi * 32, S);
+#pragma unroll
+          for (int mi = 0; mi < LIVE; ++mi)
+#pragma unroll
+            for (int ni = 0; ni < C::MFN; ++ni)
+              acc[mi][ni] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                  bf[ni], af[mi], acc[mi][ni], 0, 0, 2 * S, bs[ni], 2 * S, as[mi]);
+        };
+        step(std::integral_constant<int, 0>{});
+        step(std::integral_constant<int, 1>{});
+      }
+    }
+  };
+  // (a wave without rows only loads; each case is a loop of its own)
+  const int live = r1 - r0 - wm * C::WTM;
+  constexpr int HALF_M = (C::MFM + 1) / 2;
+  if (live > 32 * HALF_M) contract(std::integral_constant<int, C::MFM>{});
+  else if (live > 32) contract(std::integral_constant<int, HALF_M>{});
+  else if (live > 0) contract(std::integral_constant<int, 1>{});
+  else contract(std::integral_constant<int, 0>{});
 
   // ---- epilogue; acc[mi][ni][4 q + r]: row mi * 32 + lrow, column nbase + 8 q + 4 khalf + r
   const int nrows = r1 - r0;
@@ -310,6 +314,34 @@ __global__ __launch_bounds__(C::NTHR, 1) void mx_tile_kernel(MxArgs a) {
       }
     }
   }
+}
+
+// Row tiles as in the bfloat16 training products: 256 rows while an expert has
+// them, a last tile of at most 128 or 64 rows in a shape with a third stage, and
+// those behind the expert's other tiles.
+using MxT256 = MxCfg<256, 256, 2, 2, 4>;
+using MxT128 = MxCfg<128, 256, 3, 2, 4>;
+using MxT64 = MxCfg<64, 256, 3, 2, 4>;
+constexpr int MX_TM = MxT256::TM, MX_TN = MxT256::TN;
+constexpr int MX_LDS = std::max({MxT256::LDS, MxT128::LDS, MxT64::LDS});
+
+template <bool SWIGLU, bool OUT_BF16, bool GATHER>
+__global__ __launch_bounds__(512, 2) void mx_tile_kernel(MxArgs a) {
+  extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
+  constexpr int COLS = SWIGLU ? MX_TN / 2 : MX_TN;
+  const int NT = (a.N + COLS - 1) / COLS;
+  TileScan scan;
+  scan.init(a.offsets, a.E, MX_TM, a.max_rows);
+  int b = blockIdx.x;
+  const int n_active = scan.total * NT, per = n_active >> 3;
+  if (b >= n_active) return;
+  if (b < per * 8) b = (b & 7) * per + (b >> 3);       // contiguous numbers share an XCD's L2
+  const RowTile t = scan.find(a.offsets, a.E, MX_TM, a.max_rows, b / NT);
+  const TileOrder o = tile_order(t.end - t.off, MX_TM, NT, b - t.first * NT);
+  const int r0 = t.off + o.m * MX_TM, r1 = min(r0 + MX_TM, t.end), n0 = o.n * COLS;
+  if (r1 - r0 > 128) mx_tile<MxT256, SWIGLU, OUT_BF16, GATHER>(a, smem, t.e, r0, r1, n0);
+  else if (r1 - r0 > 64) mx_tile<MxT128, SWIGLU, OUT_BF16, GATHER>(a, smem, t.e, r0, r1, n0);
+  else mx_tile<MxT64, SWIGLU, OUT_BF16, GATHER>(a, smem, t.e, r0, r1, n0);
 }
 
 // ---------------------------------------------------------------------------
@@ -514,24 +546,21 @@ __global__ __launch_bounds__(512, 4) void mx_direct_kernel(MxArgs a) {
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-using MxBig = MxCfg<256, 256, 2, 2, 4>;
-using MxMed = MxCfg<128, 256, 3, 2, 4>;
-
 static long long mx_row_tiles(int max_rows, int E, int BM) {
   const long long bound = ((long long)max_rows + (long long)E * (BM - 1)) / BM;
   return bound < max_rows ? bound : max_rows;
 }
 
-template <class C, bool SWIGLU, bool OUT_BF16, bool GATHER>
+template <bool SWIGLU, bool OUT_BF16, bool GATHER>
 static hipError_t launch_mx_tile_t(const MxArgs& a, hipStream_t st) {
   static std::atomic<uint64_t> lds_set{0};
   hipError_t err = ensure_lds_limit(
-      reinterpret_cast<const void*>(&mx_tile_kernel<C, SWIGLU, OUT_BF16, GATHER>), C::LDS, lds_set);
+      reinterpret_cast<const void*>(&mx_tile_kernel<SWIGLU, OUT_BF16, GATHER>), MX_LDS, lds_set);
   if (err != hipSuccess) return err;
-  constexpr int cols = SWIGLU ? C::TN / 2 : C::TN;
-  const long long grid = mx_row_tiles(a.max_rows, a.E, C::TM) * ((a.N + cols - 1) / cols);
+  constexpr int cols = SWIGLU ? MX_TN / 2 : MX_TN;
+  const long long grid = mx_row_tiles(a.max_rows, a.E, MX_TM) * ((a.N + cols - 1) / cols);
   if (grid > INT32_MAX) return hipErrorInvalidValue;
-  mx_tile_kernel<C, SWIGLU, OUT_BF16, GATHER><<<(unsigned)grid, C::NTHR, C::LDS, st>>>(a);
+  mx_tile_kernel<SWIGLU, OUT_BF16, GATHER><<<(unsigned)grid, 512, MX_LDS, st>>>(a);
   return hipGetLastError();
 }
 
@@ -563,9 +592,8 @@ static hipError_t launch_mx_direct_t(const MxArgs& a, hipStream_t st) {
 // 1 MB of weights per CU; a contraction of one or two steps gains nothing from
 // its pipeline; and the direct kernel's 16-row tiles read the weights again
 // for every 16 rows.
-enum MxKernel { MX_K_DIRECT, MX_K_MED, MX_K_BIG };
 struct MxPlan {
-  MxKernel up, down;
+  bool up_direct, down_direct;
   int cw_up, cw_down;     // direct kernels: column groups per block
   bool h_float;           // h in float32 between the products
 };
@@ -575,33 +603,21 @@ static MxPlan mx_plan(int max_rows, int E, int H, int I) {
   // experts with rows, were every row's expert drawn alike, and their row tiles
   const double touched = E * (1.0 - __builtin_pow(1.0 - 1.0 / E, (double)max_rows));
   const double tiles = std::max(touched, max_rows / 128.0);
-  const MxKernel tiled = mean < 384 ? MX_K_MED : MX_K_BIG;
   const bool few = mean <= 64;
-  p.up = few && tiles * ((I + 127) / 128) < 160 ? MX_K_DIRECT : tiled;
-  p.down = few && (I <= 256 || tiles * ((H + 255) / 256) < 256) ? MX_K_DIRECT : tiled;
+  p.up_direct = few && tiles * ((I + 127) / 128) < 160;
+  p.down_direct = few && (I <= 256 || tiles * ((H + 255) / 256) < 256);
   const int steps = (I + 127) / 128;
   p.cw_down = steps <= 16 ? 8 : steps <= 48 ? 4 : 2;
   p.cw_up = 4;
-  if (p.up == MX_K_DIRECT && p.down == MX_K_DIRECT && I <= MXD_MAX_LDS_K)
+  if (p.up_direct && p.down_direct && I <= MXD_MAX_LDS_K)
     p.cw_up = touched * (I / 8) < 1024 ? 1 : 2;
-  p.h_float = p.up == MX_K_DIRECT && p.cw_up < 4;
+  p.h_float = p.up_direct && p.cw_up < 4;
   return p;
-}
-
-template <bool SWIGLU, bool OUT_BF16>
-static hipError_t launch_mx_tiled(const MxArgs& a, MxKernel k, hipStream_t st) {
-  if constexpr (SWIGLU) {
-    if (a.src_token)
-      return k == MX_K_BIG ? launch_mx_tile_t<MxBig, true, true, true>(a, st)
-                           : launch_mx_tile_t<MxMed, true, true, true>(a, st);
-  }
-  return k == MX_K_BIG ? launch_mx_tile_t<MxBig, SWIGLU, OUT_BF16, false>(a, st)
-                       : launch_mx_tile_t<MxMed, SWIGLU, OUT_BF16, false>(a, st);
 }
 
 template <bool OUT_BF16>
 static hipError_t launch_mx_down(const MxArgs& a, const MxPlan& p, hipStream_t st) {
-  if (p.down != MX_K_DIRECT) return launch_mx_tiled<false, OUT_BF16>(a, p.down, st);
+  if (!p.down_direct) return launch_mx_tile_t<false, OUT_BF16, false>(a, st);
   if (p.h_float) return launch_mx_direct_t<MX_DOWN32, OUT_BF16, 8>(a, st);   // I is short there
   return p.cw_down == 8   ? launch_mx_direct_t<MX_DOWN, OUT_BF16, 8>(a, st)
          : p.cw_down == 4 ? launch_mx_direct_t<MX_DOWN, OUT_BF16, 4>(a, st)
@@ -615,10 +631,11 @@ hipError_t launch_mx_ffn(const MxFfn& f, hipStream_t st) {
   const int pH = (f.H + 127) / 128 * 4, pI = (f.I + 127) / 128 * 4;
   const MxArgs up{f.x8, f.x_scale, f.src_token, f.offsets, f.E, f.max_rows, f.w13, f.w13_scale,
                   f.H, f.I, 2 * f.I, pH, pI, f.h8, f.h_scale};
-  const hipError_t err = p.up != MX_K_DIRECT ? launch_mx_tiled<true, true>(up, p.up, st)
-                         : p.cw_up == 1      ? launch_mx_direct_t<MX_UP, true, 1>(up, st)
-                         : p.cw_up == 2      ? launch_mx_direct_t<MX_UP, true, 2>(up, st)
-                                             : launch_mx_direct_t<MX_UP, true, 4>(up, st);
+  const hipError_t err = !p.up_direct  ? f.src_token ? launch_mx_tile_t<true, true, true>(up, st)
+                                                     : launch_mx_tile_t<true, true, false>(up, st)
+                         : p.cw_up == 1 ? launch_mx_direct_t<MX_UP, true, 1>(up, st)
+                         : p.cw_up == 2 ? launch_mx_direct_t<MX_UP, true, 2>(up, st)
+                                        : launch_mx_direct_t<MX_UP, true, 4>(up, st);
   if (err != hipSuccess) return err;
   const MxArgs down{f.h8, f.h_scale, nullptr, f.offsets, f.E, f.max_rows, f.w2, f.w2_scale,
                     f.I, f.H, f.H, pI, 0, f.y, nullptr};

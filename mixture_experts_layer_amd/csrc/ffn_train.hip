@@ -560,22 +560,8 @@ __global__ __launch_bounds__(512, 2) void train_rows_kernel(GemmArgs a) {
   if (b >= n_active) return;
   if (b < per * 8) b = (b & 7) * per + (b >> 3);       // contiguous numbers share an XCD's L2
   const RowTile t = scan.find(a.offsets, a.E, GEMM_TM, a.max_rows, b / NT);
-  // An expert's tiles of 129 rows and more first, then its short last tile: a
-  // CU left with a short one at the end waits less.  Within them, the 32 blocks
-  // of an XCD take all row tiles of a column while they are few, else 4 columns
-  // side by side (one column of 32 row tiles ran 10-25% slower).
-  const int rows = t.end - t.off, te = (rows + GEMM_TM - 1) / GEMM_TM;
-  const int li = b - t.first * NT, last = rows - (te - 1) * GEMM_TM;
-  const int tall = last > 128 ? te : te - 1;
-  int m_t = te - 1, n_t = li - tall * NT;
-  if (n_t < 0) {
-    const int group = tall > 8 ? 4 : 1;
-    const int g = li / (tall * group), rem = li - g * tall * group, Gc = min(group, NT - g * group);
-    m_t = rem / Gc;
-    n_t = g * group + (rem - m_t * Gc);
-  }
-  const int n0 = n_t * COLS;
-  const int r0 = t.off + m_t * GEMM_TM, r1 = min(r0 + GEMM_TM, t.end);
+  const TileOrder o = tile_order(t.end - t.off, GEMM_TM, NT, b - t.first * NT);
+  const int r0 = t.off + o.m * GEMM_TM, r1 = min(r0 + GEMM_TM, t.end), n0 = o.n * COLS;
   if (r1 - r0 > 128) gemm_tile<GemmT256, false, BKC, EPI, GATHER>(a, smem, t.e, r0, r1, n0, a.K, 0);
   else if (r1 - r0 > 64) gemm_tile<GemmT128, false, BKC, EPI, GATHER>(a, smem, t.e, r0, r1, n0, a.K, 0);
   else gemm_tile<GemmT64, false, BKC, EPI, GATHER>(a, smem, t.e, r0, r1, n0, a.K, 0);

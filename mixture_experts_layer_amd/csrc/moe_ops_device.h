@@ -195,4 +195,22 @@ struct TileScan {
   }
 };
 
+// Which tile block `li` of an expert's ceil(rows / TM) x NT tiles computes.  Row
+// tiles of more than TM / 2 rows first, the short last one behind them: a CU left
+// with a short tile at the end waits less.  Within the first, the 32 blocks of an
+// XCD take all row tiles of a column while they are few, else 4 columns side by
+// side (one column of 32 row tiles ran 10-25% slower).
+struct TileOrder {
+  int m, n;
+};
+__device__ __forceinline__ TileOrder tile_order(int rows, int TM, int NT, int li) {
+  const int te = (rows + TM - 1) / TM, last = rows - (te - 1) * TM;
+  const int tall = last > TM / 2 ? te : te - 1;
+  if (li >= tall * NT) return TileOrder{te - 1, li - tall * NT};
+  const int group = tall > 8 ? 4 : 1;
+  const int g = li / (tall * group), rem = li - g * tall * group, Gc = min(group, NT - g * group);
+  const int m = rem / Gc;
+  return TileOrder{m, g * group + (rem - m * Gc)};
+}
+
 }  // namespace moe
