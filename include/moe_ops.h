@@ -10,8 +10,9 @@
  * checked on the host before anything is enqueued, the same status codes, and
  * bitwise repeatable results (no atomics).  All pointers belong to the device
  * that is current at the call, and `stream` to that device.  A workspace
- * holds nothing between calls: it need not be initialised, and calls that
- * share one must be ordered.  Outputs must not overlap inputs or one another
+ * holds nothing between calls: it need not be initialised, calls that share
+ * one must be ordered, and one sized for max_rows (or T) rows serves every
+ * call with fewer.  Outputs must not overlap inputs or one another
  * except where a call says so.  Rows past the last expert's row are not
  * touched in any output.
  *
@@ -51,8 +52,11 @@ extern "C" {
  *   x, residual, sum, y: [T][H] dtype dt; weight[H] dtype dt; rstd[T] float32.
  *   y8[T][H] and y8_scale[T][MOE_MX_PITCH(H)]: MXFP8 of y before y's own
  *   rounding (for moe_grouped_ffn_mxfp8; the router takes y).  sum, y, y8 with
- *   y8_scale, and rstd may each be NULL, but not all of them.  sum may be x or
- *   residual itself.  eps >= 0 and finite.  H a multiple of 32, at most 16384.
+ *   y8_scale, and rstd may each be NULL, but not all of them.  sum and y may be
+ *   x or residual themselves (and not each other).  eps >= 0 and finite; with
+ *   eps = 0 a row of zeros has no norm and gives NaN.  H a multiple of 32, at
+ *   most 16384, and T * min(H / 8, 1024) below 2^32 (more rows:
+ *   MOE_ERR_UNSUPPORTED).
  */
 int moe_rmsnorm(const void* x, const void* residual, const void* weight, float eps, int T, int H,
                 int dt, void* sum, void* y, void* y8, uint8_t* y8_scale, float* rstd, void* stream);
@@ -82,7 +86,7 @@ int moe_rmsnorm_backward(const void* dy, const void* dsum, const void* s, const 
  *   and dtopk_w[t][j] = 0 where dst_row[t][j] < 0.  The gradient of y_shared
  *   is dy itself.  dst_row names every row at most once, as moe_permute writes
  *   it; rows it does not name keep what dy_perm held.  dy_perm may be y_perm
- *   itself.  Limits of moe_combine, and H at most 16384.
+ *   itself.  Limits of moe_combine, and H and T as for moe_rmsnorm.
  */
 int moe_combine_backward(const void* dy, int dt, const void* y_perm, int y_perm_dt,
                          const int32_t* dst_row, const float* topk_w, int T, int k, int H,

@@ -592,6 +592,7 @@ static hipError_t launch_mx_direct_t(const MxArgs& a, hipStream_t st) {
 // 1 MB of weights per CU; a contraction of one or two steps gains nothing from
 // its pipeline; and the direct kernel's 16-row tiles read the weights again
 // for every 16 rows.
+constexpr int MX_MIN_BLOCKS = 160;    // gate/up tiles below which the direct kernel streams faster
 struct MxPlan {
   bool up_direct, down_direct;
   int cw_up, cw_down;     // direct kernels: column groups per block
@@ -604,7 +605,7 @@ static MxPlan mx_plan(int max_rows, int E, int H, int I) {
   const double touched = E * (1.0 - __builtin_pow(1.0 - 1.0 / E, (double)max_rows));
   const double tiles = std::max(touched, max_rows / 128.0);
   const bool few = mean <= 64;
-  p.up_direct = few && tiles * ((I + 127) / 128) < 160;
+  p.up_direct = few && tiles * ((I + 127) / 128) < MX_MIN_BLOCKS;
   p.down_direct = few && (I <= 256 || tiles * ((H + 255) / 256) < 256);
   const int steps = (I + 127) / 128;
   p.cw_down = steps <= 16 ? 8 : steps <= 48 ? 4 : 2;
@@ -624,7 +625,9 @@ static hipError_t launch_mx_down(const MxArgs& a, const MxPlan& p, hipStream_t s
                           : launch_mx_direct_t<MX_DOWN, OUT_BF16, 2>(a, st);
 }
 
-bool mx_h_is_float(int max_rows, int E, int H, int I) { return mx_plan(max_rows, E, H, I).h_float; }
+// h is float32 only under a direct up kernel, so with fewer than
+// MX_MIN_BLOCKS / ceil(I / 128) row tiles, which max_rows / 128 never exceeds.
+size_t mx_float_rows(int I) { return (size_t)128 * MX_MIN_BLOCKS / ((I + 127) / 128); }
 
 hipError_t launch_mx_ffn(const MxFfn& f, hipStream_t st) {
   const MxPlan p = mx_plan(f.max_rows, f.E, f.H, f.I);

@@ -16,6 +16,7 @@ constexpr int OPS_MAX_H = 16384;   // row elements the one-block-per-row kernels
 hipError_t launch_zero(void* p, size_t bytes, hipStream_t st);
 
 // norm.hip; H a multiple of 32, at most OPS_MAX_H
+int row_threads(int H);            // threads of the block that takes a row
 hipError_t launch_rmsnorm(const void* x, const void* residual, const void* w, float eps, int T,
                           int H, int dt, void* sum, void* y, void* y8, void* y8_scale, float* rstd,
                           hipStream_t st);
@@ -58,12 +59,12 @@ struct MxFfn {
   const uint8_t* w2;
   const uint8_t* w2_scale;
   uint8_t* h8;              // workspace: h [max_rows][I] in e4m3 and its scales,
-                            // or in float32 where mx_h_is_float
+                            // or in float32 (mx_float_rows at most)
   uint8_t* h_scale;
   void* y;
   int y_dt;
 };
-bool mx_h_is_float(int max_rows, int E, int H, int I);
+size_t mx_float_rows(int I);        // most rows whose h is kept in float32
 hipError_t launch_mx_ffn(const MxFfn& f, hipStream_t st);
 
 }  // namespace moe

@@ -328,7 +328,7 @@ hipError_t launch_zero(void* p, size_t bytes, hipStream_t st) {
 
 // Threads per row and 8-element chunks per thread: one chunk per thread up to
 // 8192 elements, two beyond (the block limit of 1024 threads).
-static int row_threads(int H) {
+int row_threads(int H) {
   const int n = H / 8;
   return n >= 1024 ? 1024 : (n + 63) / 64 * 64;
 }

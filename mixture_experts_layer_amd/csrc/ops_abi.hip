@@ -26,6 +26,8 @@ int check_row_width(int H) {
   if (st) return st;
   return H > OPS_MAX_H ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
+// A block per row: a launch holds fewer than 2^32 threads.
+bool rows_fit(int T, int H) { return (long long)T * row_threads(H) < (1ll << 32); }
 
 // Shapes of an expert block beside the layer's own.
 int check_block(int max_rows, int E_loc, int H, int I_loc) {
@@ -48,6 +50,7 @@ int moe_rmsnorm(const void* x, const void* residual, const void* weight, float e
   if (!valid_dt(dt) || T < 0 || !(eps >= 0.f) || std::isinf(eps)) return MOE_ERR_INVALID_ARG;
   const int st = check_row_width(H);
   if (st) return st;
+  if (!rows_fit(T, H)) return MOE_ERR_UNSUPPORTED;
   if (!y8 != !y8_scale) return MOE_ERR_INVALID_ARG;
   if (!sum && !y && !y8 && !rstd) return MOE_ERR_INVALID_ARG;
   if (any_misaligned(x, residual, weight, sum, y, y8, y8_scale, rstd)) return MOE_ERR_INVALID_ARG;
@@ -82,7 +85,7 @@ int moe_combine_backward(const void* dy, int dt, const void* y_perm, int y_perm_
   if (!valid_dt(dt) || !valid_dt(y_perm_dt) || T < 0 || k < 1) return MOE_ERR_INVALID_ARG;
   const int st = check_row_width(H);
   if (st) return st;
-  if (k > KMAX || !fits_int(T, k)) return MOE_ERR_UNSUPPORTED;
+  if (k > KMAX || !fits_int(T, k) || !rows_fit(T, H)) return MOE_ERR_UNSUPPORTED;
   if (any_misaligned(dy, y_perm, dst_row, topk_w, dy_perm, dtopk_w)) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   if (!dy || !y_perm || !dst_row || !topk_w || !dy_perm || !dtopk_w) return MOE_ERR_INVALID_ARG;
@@ -155,8 +158,13 @@ int moe_grouped_ffn_backward(const void* dy_perm, const void* x_perm, const void
 size_t moe_grouped_ffn_mxfp8_workspace_size(int max_rows, int E_loc, int H, int I_loc) {
   if (check_block(max_rows, E_loc, H, I_loc) != MOE_OK) return 0;
   const size_t rows = max_rows > 0 ? max_rows : 1;
-  if (mx_h_is_float(max_rows, E_loc, H, I_loc)) return align_up(rows * I_loc * 4);
-  return align_up(rows * I_loc) + align_up(rows * MOE_MX_PITCH(I_loc));
+  // h in MXFP8, or in float32 where few rows take that form: the larger of the
+  // two for any count up to max_rows, so that a program's largest batch sizes
+  // the workspace for all
+  const size_t f = rows < mx_float_rows(I_loc) ? rows : mx_float_rows(I_loc);
+  const size_t h8 = align_up(rows * I_loc) + align_up(rows * MOE_MX_PITCH(I_loc));
+  const size_t hf = align_up(f * I_loc * 4);
+  return h8 > hf ? h8 : hf;
 }
 
 int moe_grouped_ffn_mxfp8(const void* x8, const uint8_t* x_scale, const int32_t* src_token,

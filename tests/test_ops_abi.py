@@ -188,3 +188,62 @@ def test_mxfp8_workspace_and_no_rows():
         assert q(*bad) == 0
     none = {n: None for n in ("x8", "x_scale", "offsets", "w13", "w13_scale", "w2", "w2_scale", "y_perm", "ws")}
     assert _st("moe_grouped_ffn_mxfp8", *dict(MX, max_rows=0, **none).values()) == 0
+
+
+def test_more_rows_than_a_launch_holds_are_refused():
+    assert _st("moe_rmsnorm", *dict(NORM, T=2 ** 22, H=8192).values()) == UNSUPPORTED
+    assert _st("moe_combine_backward", *dict(COMBINE, T=2 ** 22, H=8192, k=1).values()) == UNSUPPORTED
+
+
+def test_a_workspace_for_the_largest_batch_serves_all():
+    import random
+    rng = random.Random(7)
+    for q, tail in ((M.moe_grouped_ffn_mxfp8_workspace_size, ()), (M.moe_grouped_ffn_train_workspace_size, (1,)),
+                    (M.moe_grouped_ffn_backward_workspace_size, (1,))):
+        for _ in range(400):
+            E, H, I = rng.choice([1, 8, 60, 128, 1024]), 32 * rng.randint(1, 256), 32 * rng.randint(1, 256)
+            a, b = sorted(int(2 ** rng.uniform(0, 20)) for _ in range(2))
+            assert 0 < q(a, E, H, I, *tail) <= q(b, E, H, I, *tail), (a, b, E, H, I)
+    sizes = [M.moe_rmsnorm_backward_workspace_size(T, 4096, 1) for T in range(1, 2000, 7)]
+    assert sizes == sorted(sizes)
+
+
+class _OnDevice(torch.Tensor):
+    """A CPU tensor that says it lives on a GPU, for the binding's own logic."""
+
+    @staticmethod
+    def __new__(cls, t, device):
+        self = torch.Tensor._make_subclass(cls, t)
+        self.where = device
+        return self
+
+    def get_device(self):
+        return self.where
+
+
+def test_the_binding_runs_on_the_tensors_device(monkeypatch):
+    """Tensors of another GPU than the current one: the call is made with that
+    GPU current and on its current stream; tensors of two GPUs are refused."""
+    from contextlib import contextmanager
+    from types import SimpleNamespace
+
+    from mixture_experts_layer_amd import ops
+    current, seen = [0], []
+
+    @contextmanager
+    def device(d):
+        old, current[0] = current[0], d
+        yield
+        current[0] = old
+    stub = SimpleNamespace(Tensor=torch.Tensor, cuda=SimpleNamespace(current_device=lambda: current[0], device=device),
+                           _C=SimpleNamespace(_cuda_getCurrentRawStream=lambda d: 1000 + d))
+    monkeypatch.setattr(ops, "_TORCH", stub)
+    monkeypatch.setattr(ops, "_TYPES", {"f": (torch.float32,)})
+    monkeypatch.setattr(ops, "_LIB", SimpleNamespace(f=lambda *a: seen.append((current[0], a[-1])) or 0))
+    t0, t1 = _OnDevice(torch.zeros(4), 0), _OnDevice(torch.zeros(4), 1)
+    ops._call("f", (("a", t0, "f", 4),), (t0,), None)
+    ops._call("f", (("a", t1, "f", 4),), (t1,), None)
+    ops._call("f", (("a", t1, "f", 4),), (t1,), 77)
+    assert seen == [(0, 1000), (1, 1001), (1, 77)] and current[0] == 0
+    with pytest.raises(ValueError, match="not cuda:0"):
+        ops._call("f", (("a", t0, "f", 4), ("b", t1, "f", 4)), (t0, t1), None)
