@@ -640,7 +640,8 @@ __global__ __launch_bounds__(256) void train_gather_kernel(const uint4* x, const
 // The float32 layer is small (the toy layer has 16 rows per expert), so a
 // block takes 32 x 32 outputs and its 4 waves split the contraction in
 // interleaved chunks of 16, each with the next chunk's loads in flight; they
-// meet in LDS in wave order.  A lane's four elements of a chunk feed four
+// meet in LDS in wave order.  (WAVES: a wave takes 32 x 32 outputs of a weight
+// gradient alone, where a few rows per expert leave nothing to split.)  A lane's four elements of a chunk feed four
 // products: element i of lane l stands for k = 4 (l / 16) + i in both operands.
 // (64 x 64 tiles of plain multiply-adds: 343 us for the toy layer's step.)
 // ---------------------------------------------------------------------------
@@ -659,18 +660,21 @@ struct F32GemmArgs {
 
 constexpr int F32_T = 32;
 
-template <bool WGRAD, bool BKC, int EPI>
-__device__ __forceinline__ void f32_tile(const F32GemmArgs& a, int block) {
+constexpr int f32_lds(int EPI) { return 4 * F32_T * ((EPI == EPI_SWIGLU ? 4 : 2) * 16 + 4); }
+
+template <bool WGRAD, bool BKC, int EPI, bool WAVES>
+__device__ __forceinline__ void f32_tile(const F32GemmArgs& a, int block, float* lds) {
   constexpr int T = F32_T, NB = EPI == EPI_SWIGLU ? 4 : 2;    // 16-column operands (gate, then up)
   constexpr int PITCH = NB * 16 + 4;
-  __shared__ __attribute__((aligned(16))) float red[4][T][PITCH];
+  auto red = reinterpret_cast<float(*)[T][PITCH]>(lds);
   const int lane = threadIdx.x & 63;
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int NT = a.N / T, n0 = (block % NT) * T;
+  const int NT = a.N / T, tile = WAVES ? block * 4 + wid : block, n0 = (tile % NT) * T;
   int e, r0, r1, K, krow0 = 0;
   if constexpr (WGRAD) {
-    const int MT = a.M / T, li = block / NT;
+    const int MT = a.M / T, li = tile / NT;
     e = li / MT;
+    if (e >= a.E) return;
     r0 = (li - e * MT) * T;
     r1 = r0 + T;
     const int o = a.offsets[e];
@@ -679,11 +683,11 @@ __device__ __forceinline__ void f32_tile(const F32GemmArgs& a, int block) {
   } else {
     TileScan scan;
     scan.init(a.offsets, a.E, T, a.max_rows);
-    const int tile = block / NT;
-    if (tile >= scan.total) return;
-    const RowTile t = scan.find(a.offsets, a.E, T, a.max_rows, tile);
+    const int m_t = tile / NT;
+    if (m_t >= scan.total) return;
+    const RowTile t = scan.find(a.offsets, a.E, T, a.max_rows, m_t);
     e = t.e;
-    r0 = t.off + (tile - t.first) * T;
+    r0 = t.off + (m_t - t.first) * T;
     r1 = min(r0 + T, t.end);
     K = a.K;
   }
@@ -749,17 +753,28 @@ __device__ __forceinline__ void f32_tile(const F32GemmArgs& a, int block) {
           acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(c.b[j][q], c.a[i][q], acc[i][j], 0, 0, 0);
   };
   const int steps = (K + 15) / 16;
+  constexpr int ds = WAVES ? 1 : 4;
   Chunk16 c0, c1;
-  int s = wid;
+  int s = WAVES ? 0 : wid;
   if (s < steps) load(c0, s);
-  for (; s < steps; s += 8) {
-    if (s + 4 < steps) load(c1, s + 4);
+  for (; s < steps; s += 2 * ds) {
+    if (s + ds < steps) load(c1, s + ds);
     multiply(c0);
-    if (s + 4 >= steps) break;
-    if (s + 8 < steps) load(c0, s + 8);
+    if (s + ds >= steps) break;
+    if (s + 2 * ds < steps) load(c0, s + 2 * ds);
     multiply(c1);
   }
+  float* out = WGRAD ? a.out + (size_t)e * a.out_stride : a.out;
   // lane l holds columns 4 (l / 16) + [0, 4) of row l % 16 of every operand pair
+  if constexpr (WAVES) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        *reinterpret_cast<float4*>(out + (size_t)(r0 + 16 * i + lr) * a.ldo + n0 + 16 * j + 4 * lg) =
+            make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -767,7 +782,6 @@ __device__ __forceinline__ void f32_tile(const F32GemmArgs& a, int block) {
       *reinterpret_cast<float4*>(&red[wid][16 * i + lr][16 * j + 4 * lg]) =
           make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
   __syncthreads();
-  float* out = WGRAD ? a.out + (size_t)e * a.out_stride : a.out;
   for (int o = threadIdx.x; o < T * T; o += 256) {
     const int m = o / T, n = o % T, row = r0 + m, col = n0 + n;
     if (row >= r1) continue;
@@ -796,16 +810,19 @@ __device__ __forceinline__ void f32_tile(const F32GemmArgs& a, int block) {
 
 template <bool BKC, int EPI>
 __global__ __launch_bounds__(256) void train_f32_kernel(F32GemmArgs a) {
-  f32_tile<false, BKC, EPI>(a, blockIdx.x);
+  __shared__ __attribute__((aligned(16))) float lds[f32_lds(EPI)];
+  f32_tile<false, BKC, EPI, false>(a, blockIdx.x, lds);
 }
 // dx, dW13 and dW2, which need dh's results but not one another's, in one
 // launch: blocks from 0, from b13 and from b2 on.
+template <bool WAVES>
 __global__ __launch_bounds__(256) void train_f32_grads_kernel(F32GemmArgs ax, F32GemmArgs a13,
                                                               F32GemmArgs a2, int b13, int b2) {
+  __shared__ __attribute__((aligned(16))) float lds[f32_lds(EPI_STORE)];
   const int b = blockIdx.x;
-  if (b < b13) f32_tile<false, false, EPI_STORE>(ax, b);
-  else if (b < b2) f32_tile<true, false, EPI_STORE>(a13, b - b13);
-  else f32_tile<true, false, EPI_STORE>(a2, b - b2);
+  if (b < b13) f32_tile<false, false, EPI_STORE, false>(ax, b, lds);
+  else if (b < b2) f32_tile<true, false, EPI_STORE, WAVES>(a13, b - b13, lds);
+  else f32_tile<true, false, EPI_STORE, WAVES>(a2, b - b2, lds);
 }
 
 // ---------------------------------------------------------------------------
@@ -821,8 +838,9 @@ static long long cdivl(long long a, long long b) { return (a + b - 1) / b; }
 static long long f32_row_blocks(const F32GemmArgs& a) {
   return row_tiles(a.max_rows, a.E, F32_T) * (a.N / F32_T);
 }
-static long long f32_wgrad_blocks(const F32GemmArgs& a) {
-  return (long long)a.E * (a.M / F32_T) * (a.N / F32_T);
+static long long f32_wgrad_blocks(const F32GemmArgs& a, bool waves) {
+  const long long tiles = (long long)a.E * (a.M / F32_T) * (a.N / F32_T);
+  return waves ? cdivl(tiles, 4) : tiles;
 }
 
 template <bool BKC, int EPI, bool GATHER>
@@ -913,11 +931,17 @@ hipError_t launch_train_backward(const TrainFfn& f, const void* dy, void* dgu, v
   if (err != hipSuccess) return err;
   if (f.dt == 0) {
     // the rest in one launch
+    // Few rows per expert: a wave per tile of a weight gradient (4 and 64 rows
+    // for each of 64 experts, H 1024, I 512, the step: 582 -> 355 and 890 -> 790
+    // us).  Many rows or few tiles: four waves split the rows (8 experts of 1024
+    // rows 412 -> 392 us; one of 1024, H = I = 64, 110 -> 42).
+    const bool waves = f.max_rows <= 64ll * f.E;
     const F32GemmArgs ax = f32_args(f, pdx), a13 = f32_args(f, p13), a2 = f32_args(f, p2);
-    const long long gx = dx ? f32_row_blocks(ax) : 0, g13 = dw13 ? f32_wgrad_blocks(a13) : 0;
-    const long long grid = gx + g13 + (dw2 ? f32_wgrad_blocks(a2) : 0);
+    const long long gx = dx ? f32_row_blocks(ax) : 0, g13 = dw13 ? f32_wgrad_blocks(a13, waves) : 0;
+    const long long grid = gx + g13 + (dw2 ? f32_wgrad_blocks(a2, waves) : 0);
     if (grid > INT32_MAX) return hipErrorInvalidValue;
-    train_f32_grads_kernel<<<(unsigned)grid, 256, 0, st>>>(ax, a13, a2, (int)gx, (int)(gx + g13));
+    (waves ? train_f32_grads_kernel<true> : train_f32_grads_kernel<false>)<<<
+        (unsigned)grid, 256, 0, st>>>(ax, a13, a2, (int)gx, (int)(gx + g13));
     return hipGetLastError();
   }
   if (dx && (err = rows_product<false, EPI_STORE>(f, pdx, st)) != hipSuccess) return err;
