@@ -330,15 +330,9 @@ __global__ __launch_bounds__(512, 2) void mx_tile_kernel(MxArgs a) {
   extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
   constexpr int COLS = SWIGLU ? MX_TN / 2 : MX_TN;
   const int NT = (a.N + COLS - 1) / COLS;
-  TileScan scan;
-  scan.init(a.offsets, a.E, MX_TM, a.max_rows);
-  int b = blockIdx.x;
-  const int n_active = scan.total * NT, per = n_active >> 3;
-  if (b >= n_active) return;
-  if (b < per * 8) b = (b & 7) * per + (b >> 3);       // contiguous numbers share an XCD's L2
-  const RowTile t = scan.find(a.offsets, a.E, MX_TM, a.max_rows, b / NT);
-  const TileOrder o = tile_order(t.end - t.off, MX_TM, NT, b - t.first * NT);
-  const int r0 = t.off + o.m * MX_TM, r1 = min(r0 + MX_TM, t.end), n0 = o.n * COLS;
+  RowBlock t;
+  if (!row_block<MX_TM>(a.offsets, a.E, a.max_rows, NT, blockIdx.x, t)) return;
+  const int r0 = t.r0, r1 = t.r1, n0 = t.n * COLS;
   if (r1 - r0 > 128) mx_tile<MxT256, SWIGLU, OUT_BF16, GATHER>(a, smem, t.e, r0, r1, n0);
   else if (r1 - r0 > 64) mx_tile<MxT128, SWIGLU, OUT_BF16, GATHER>(a, smem, t.e, r0, r1, n0);
   else mx_tile<MxT64, SWIGLU, OUT_BF16, GATHER>(a, smem, t.e, r0, r1, n0);

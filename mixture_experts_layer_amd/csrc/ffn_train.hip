@@ -568,15 +568,9 @@ __global__ __launch_bounds__(512, 2) void train_rows_kernel(GemmArgs a) {
   extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
   constexpr int COLS = EPI == EPI_SWIGLU ? GEMM_TN / 2 : GEMM_TN;
   const int NT = (a.N + COLS - 1) / COLS;
-  TileScan scan;
-  scan.init(a.offsets, a.E, GEMM_TM, a.max_rows);
-  int b = blockIdx.x;
-  const int n_active = scan.total * NT, per = n_active >> 3;
-  if (b >= n_active) return;
-  if (b < per * 8) b = (b & 7) * per + (b >> 3);       // contiguous numbers share an XCD's L2
-  const RowTile t = scan.find(a.offsets, a.E, GEMM_TM, a.max_rows, b / NT);
-  const TileOrder o = tile_order(t.end - t.off, GEMM_TM, NT, b - t.first * NT);
-  const int r0 = t.off + o.m * GEMM_TM, r1 = min(r0 + GEMM_TM, t.end), n0 = o.n * COLS;
+  RowBlock t;
+  if (!row_block<GEMM_TM>(a.offsets, a.E, a.max_rows, NT, blockIdx.x, t)) return;
+  const int r0 = t.r0, r1 = t.r1, n0 = t.n * COLS;
   if (r1 - r0 > 128) gemm_tile<GemmT256, false, BKC, EPI, GATHER>(a, smem, t.e, r0, r1, n0, a.K, 0);
   else if (r1 - r0 > 64) gemm_tile<GemmT128, false, BKC, EPI, GATHER>(a, smem, t.e, r0, r1, n0, a.K, 0);
   else gemm_tile<GemmT64, false, BKC, EPI, GATHER>(a, smem, t.e, r0, r1, n0, a.K, 0);
