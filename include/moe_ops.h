@@ -85,8 +85,10 @@ int moe_rmsnorm_backward(const void* dy, const void* dsum, const void* s, const 
  *     dtopk_w[t][j] = sum_h dy[t][h] * y_perm[row][h]          (float32)
  *   and dtopk_w[t][j] = 0 where dst_row[t][j] < 0.  The gradient of y_shared
  *   is dy itself.  dst_row names every row at most once, as moe_permute writes
- *   it; rows it does not name keep what dy_perm held.  dy_perm may be y_perm
- *   itself.  Limits of moe_combine, and H and T as for moe_rmsnorm.
+ *   it; rows it does not name keep what dy_perm held (so in a padded layout,
+ *   whose blank rows moe_grouped_ffn_backward reads as well, clear dy_perm
+ *   first).  dy_perm may be y_perm itself, where no row of it is blank.
+ *   Limits of moe_combine, and H and T as for moe_rmsnorm.
  */
 int moe_combine_backward(const void* dy, int dt, const void* y_perm, int y_perm_dt,
                          const int32_t* dst_row, const float* topk_w, int T, int k, int H,
@@ -117,8 +119,10 @@ int moe_combine_backward(const void* dy, int dt, const void* y_perm, int y_perm_
  *   weights 1.  Shape limits of moe_grouped_ffn; H and I_loc at most
  *   65536 and H * I_loc at most 2^30.
  *   An expert whose offsets leave [0, max_rows] or decrease is treated as one
- *   without rows.  With src_token, every source must be a row of x (padding
- *   sources of -1 are refused by no check and read row 0).
+ *   without rows.  With src_token, every source must be a row of x; a source of
+ *   -1 reads row 0.  For the padded layout of moe_permute_capacity pass its
+ *   x_perm to both, and rows of zeros in dy_perm for its blank rows: they then
+ *   add nothing to any gradient.
  */
 size_t moe_grouped_ffn_train_workspace_size(int max_rows, int E_loc, int H, int I_loc, int dt);
 int moe_grouped_ffn_train(const void* x_perm, const void* x, const int32_t* src_token,
@@ -144,7 +148,8 @@ int moe_grouped_ffn_backward(const void* dy_perm, const void* x_perm, const void
  *   w2[E_loc][H][I_loc] with w2_scale[E_loc][H][MOE_MX_PITCH(I_loc)];
  *   y_perm[max_rows][H] of dtype y_dt.  Elements must be finite and scale
  *   bytes below 255.  Limits, offsets and sources as for
- *   moe_grouped_ffn_train.
+ *   moe_grouped_ffn_train (a source of -1 gives a meaningless row, which
+ *   moe_combine does not read).
  */
 size_t moe_grouped_ffn_mxfp8_workspace_size(int max_rows, int E_loc, int H, int I_loc);
 int moe_grouped_ffn_mxfp8(const void* x8, const uint8_t* x_scale, const int32_t* src_token,

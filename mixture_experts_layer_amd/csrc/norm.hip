@@ -140,7 +140,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(NormBwdArgs a) {
   }
   Chunk<BF16> dy[NV], s[NV], ds[NV];
   float rs = 0.f;
-  auto fetch = [&](int t) {
+  auto fetch = [&](unsigned t) {
     rs = a.rstd[t];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -152,9 +152,11 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(NormBwdArgs a) {
       }
     }
   };
-  int t = blockIdx.x, turn = 0;
-  if (t < a.T) fetch(t);
-  for (; t < a.T; t += gridDim.x, turn ^= 1) {
+  const unsigned T = a.T;      // (unsigned: the step past the last row may leave int)
+  unsigned t = blockIdx.x;
+  int turn = 0;
+  if (t < T) fetch(t);
+  for (; t < T; t += gridDim.x, turn ^= 1) {
     const float rstd = rs;
     float xh[NV][8], g[NV][8], dot = 0.f;
     Chunk<BF16> dsum[NV];
@@ -177,7 +179,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(NormBwdArgs a) {
       }
     }
     // the next row's loads fly during this row's reduction and stores
-    if (t + (int)gridDim.x < a.T) fetch(t + gridDim.x);
+    if (t + gridDim.x < T) fetch(t + gridDim.x);
     const float m = block_sum(dot, red[turn]) / (float)a.H;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {

@@ -118,6 +118,50 @@ def test_training_step(T, k):
         assert float((got.double() - ref.grad).norm()) <= tol * float(ref.grad.norm())
 
 
+# (19 rows: every expert full and pairs dropped; 122: none dropped, blank rows in
+# every expert; 26 lies between)
+@pytest.mark.parametrize("C", [19, 26, 122])
+@pytest.mark.parametrize("dt", [0, 1])
+def test_padded_and_dropped_tokens(dt, C):
+    """With a capacity, the padded layout gives the packed layout's outputs and
+    gradients (sums in another order: each within 1e-5 or, in bfloat16, 2^-7 of
+    the formula in 2-norm), dropped pairs get zero gradients, and the blank rows
+    add nothing."""
+    T, H, I, E, k = 61, 96, 64, 5, 2
+    d = [torch.float32, torch.bfloat16][dt]
+    x, w_r, G = _rand((T, H), 41, 1.0, d), _rand((E, H), 42, H ** -0.5, d), _rand((T, H), 43, 1.0, d)
+    w13, w2 = _rand((E, 2 * I, H), 44, H ** -0.5, d), _rand((E, H, I), 45, I ** -0.5, d)
+    _, ids, w, _, _, _ = _route_and_permute(x, w_r, T, H, E, k, 0, dt)
+
+    def run(padded):
+        rows = E * C if padded else T * k
+        i32 = torch.int32
+        cnt, off, src, dst, drop = _e(E, dtype=i32), _e(E + 1, dtype=i32), _e(rows, dtype=i32), _e(T, k, dtype=i32), _e(1, dtype=i32)
+        xp = _e(rows, H, dtype=d)
+        wsp = torch.empty(max(M.moe_permute_workspace_size(T, k, E), 16), device=DEV, dtype=torch.uint8)
+        M.moe_permute_capacity(ids, T, k, E, 0, E, C, padded, x, H, dt, cnt, off, src, dst, xp, drop, wsp, wsp.numel())
+        n = max(M.moe_grouped_ffn_train_workspace_size(rows, E, H, I, dt), M.moe_grouped_ffn_backward_workspace_size(rows, E, H, I, dt))
+        ws = torch.empty(n, device=DEV, dtype=torch.uint8)
+        gu, yp, out = _e(rows, 2 * I), _e(rows, H, dtype=d), _e(T, H, dtype=d)
+        M.moe_grouped_ffn_train(xp, None, None, off, E, rows, H, I, w13, w2, dt, gu, yp, ws, n)
+        M.moe_combine(yp, dt, dst, w, T, k, H, None, out, dt)
+        dyp, dw = torch.zeros(rows, H, device=DEV, dtype=d), _e(T, k)
+        M.moe_combine_backward(G, dt, yp, dt, dst, w, T, k, H, dyp, dw)
+        dxp, d13, d2 = _e(rows, H, dtype=d), torch.empty_like(w13), torch.empty_like(w2)
+        M.moe_grouped_ffn_backward(dyp, xp, None, None, off, E, rows, H, I, w13, w2, dt, gu, dxp, d13, d2, ws, n)
+        dx = _e(T, H, dtype=d)
+        M.moe_combine(dxp, dt, dst, torch.ones(T, k, device=DEV), T, k, H, None, dx, dt)
+        if padded:
+            blank = src < 0
+            assert not yp[blank].any() and not dxp[blank].any()
+            assert int(blank.sum()) == rows - int(cnt.sum()) and (C < 122 or blank.any())
+        assert not dw[dst < 0].any() and int((dst < 0).sum()) == int(drop) and (C > 19 or int(drop) > 0)
+        return out, dw, dx, d13, d2
+    for p, q in zip(run(0), run(1)):
+        p, q = p.double(), q.double()
+        assert float((p - q).norm()) <= 2 * (2.0 ** -7 if dt else 1e-5) * float(p.norm())
+
+
 def test_rows_past_2_31_elements():
     """Expert rows and their gradients beyond 32-bit element offsets: the last
     rows equal those of a small call."""
