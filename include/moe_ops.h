@@ -117,7 +117,10 @@ int moe_combine_backward(const void* dy, int dt, const void* y_perm, int y_perm_
  *   writes them for every expert.  The gradient of token t's row in the
  *   gathered form is the sum of its copies' dx_perm rows: moe_combine with
  *   weights 1.  Shape limits of moe_grouped_ffn; H and I_loc at most
- *   65536 and H * I_loc at most 2^30.
+ *   65536, H * I_loc and max_rows at most 2^30, and shapes that a launch of
+ *   fewer than 2^32 threads does not cover are MOE_ERR_UNSUPPORTED: in float32
+ *   from 1.7e10 elements of dx_perm, dw13 and dw2 together, in bfloat16 from
+ *   2^28 rows or 2.7e11 elements.
  *   An expert whose offsets leave [0, max_rows] or decrease is treated as one
  *   without rows.  With src_token, every source must be a row of x; a source of
  *   -1 reads row 0.  For the padded layout of moe_permute_capacity pass its

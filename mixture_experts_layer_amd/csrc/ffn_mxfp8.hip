@@ -545,6 +545,12 @@ static long long mx_row_tiles(int max_rows, int E, int BM) {
   return bound < max_rows ? bound : max_rows;
 }
 
+// (the direct kernel takes few rows, so fewer and smaller blocks)
+bool mx_fits(int max_rows, int E, int H, int I) {
+  const long long cols = std::max((I + MX_TN / 2 - 1) / (MX_TN / 2), (H + MX_TN - 1) / MX_TN);
+  return mx_row_tiles(max_rows, E, MX_TM) * cols * 512 < (1ll << 32);
+}
+
 template <bool SWIGLU, bool OUT_BF16, bool GATHER>
 static hipError_t launch_mx_tile_t(const MxArgs& a, hipStream_t st) {
   static std::atomic<uint64_t> lds_set{0};
@@ -594,7 +600,7 @@ struct MxPlan {
 };
 static MxPlan mx_plan(int max_rows, int E, int H, int I) {
   MxPlan p{};
-  const int mean = (max_rows + E - 1) / E;
+  const int mean = max_rows / E + (max_rows % E != 0);
   // experts with rows, were every row's expert drawn alike, and their row tiles
   const double touched = E * (1.0 - __builtin_pow(1.0 - 1.0 / E, (double)max_rows));
   const double tiles = std::max(touched, max_rows / 128.0);

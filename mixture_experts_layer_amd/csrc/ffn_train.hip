@@ -851,6 +851,21 @@ static hipError_t launch_rows(const GemmArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
+bool train_fits(int max_rows, int E, int H, int I, int dt) {
+  long long threads;
+  if (dt == 0) {
+    const long long rows = row_tiles(max_rows, E, F32_T), h = H / F32_T, i = I / F32_T;
+    threads = 256 * std::max(rows * i, rows * h + 3 * E * h * i);
+  } else {
+    const long long rows = row_tiles(max_rows, E, GEMM_TM), cols = GEMM_TN;
+    const long long row_blocks = rows * std::max(cdivl(I, cols / 2), cdivl(H, cols));
+    const long long grad_blocks = E * (cdivl(2 * I, GemmW::TM) * cdivl(H, GemmW::TN) +
+                                       cdivl(H, GemmW::TM) * cdivl(I, GemmW::TN));
+    threads = std::max(512 * std::max(row_blocks, grad_blocks), cdivl(max_rows, GR_ROWS) * 256);
+  }
+  return threads < (1ll << 32);
+}
+
 static long long wgrad_blocks(const GemmArgs& a) {
   return a.E * cdivl(a.M, GemmW::TM) * cdivl(a.N, GemmW::TN);
 }

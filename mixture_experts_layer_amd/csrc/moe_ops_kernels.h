@@ -41,6 +41,10 @@ struct TrainFfn {
 };
 constexpr int OPS_MAX_DIM = 65536;               // H and I of the expert blocks
 constexpr long long OPS_MAX_HI = 1ll << 30;      // H * I: an expert's weights within 4 GiB
+constexpr int OPS_MAX_ROWS = 1 << 30;            // rows of the expert blocks
+// whether every launch of a shape holds fewer than 2^32 threads
+bool train_fits(int max_rows, int E, int H, int I, int dt);
+bool mx_fits(int max_rows, int E, int H, int I);
 hipError_t launch_train_forward(const TrainFfn& f, void* y, hipStream_t st);
 // dgu: [max_rows][2 I], workspace; x_perm: [max_rows][H], workspace of the
 // gathered form; dx, or dw13 with dw2, may be null

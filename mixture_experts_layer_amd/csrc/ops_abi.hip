@@ -35,9 +35,20 @@ int check_block(int max_rows, int E_loc, int H, int I_loc) {
   const int st = check_hidden(H);
   if (st) return st;
   if (I_loc % 32 || E_loc > 1024 || H > OPS_MAX_DIM || I_loc > OPS_MAX_DIM ||
-      (long long)H * I_loc > OPS_MAX_HI)
+      (long long)H * I_loc > OPS_MAX_HI || max_rows > OPS_MAX_ROWS)
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
+}
+int check_train(int max_rows, int E_loc, int H, int I_loc, int dt) {
+  if (!valid_dt(dt)) return MOE_ERR_INVALID_ARG;
+  const int st = check_block(max_rows, E_loc, H, I_loc);
+  if (st) return st;
+  return train_fits(max_rows, E_loc, H, I_loc, dt) ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+int check_mx(int max_rows, int E_loc, int H, int I_loc) {
+  const int st = check_block(max_rows, E_loc, H, I_loc);
+  if (st) return st;
+  return mx_fits(max_rows, E_loc, H, I_loc) ? MOE_OK : MOE_ERR_UNSUPPORTED;
 }
 
 }  // namespace
@@ -94,7 +105,7 @@ int moe_combine_backward(const void* dy, int dt, const void* y_perm, int y_perm_
 }
 
 size_t moe_grouped_ffn_train_workspace_size(int max_rows, int E_loc, int H, int I_loc, int dt) {
-  if (!valid_dt(dt) || check_block(max_rows, E_loc, H, I_loc) != MOE_OK) return 0;
+  if (check_train(max_rows, E_loc, H, I_loc, dt) != MOE_OK) return 0;
   return align_up((size_t)(max_rows > 0 ? max_rows : 1) * I_loc * elt_bytes(dt));
 }
 
@@ -102,8 +113,7 @@ int moe_grouped_ffn_train(const void* x_perm, const void* x, const int32_t* src_
                           const int32_t* offsets, int E_loc, int max_rows, int H, int I_loc,
                           const void* w13, const void* w2, int dt, float* gu, void* y_perm,
                           void* ws, size_t ws_bytes, void* stream) {
-  if (!valid_dt(dt)) return MOE_ERR_INVALID_ARG;
-  const int st = check_block(max_rows, E_loc, H, I_loc);
+  const int st = check_train(max_rows, E_loc, H, I_loc, dt);
   if (st) return st;
   if (any_misaligned(x_perm, x, src_token, offsets, w13, w2, gu, y_perm, ws))
     return MOE_ERR_INVALID_ARG;
@@ -118,7 +128,7 @@ int moe_grouped_ffn_train(const void* x_perm, const void* x, const int32_t* src_
 }
 
 size_t moe_grouped_ffn_backward_workspace_size(int max_rows, int E_loc, int H, int I_loc, int dt) {
-  if (!valid_dt(dt) || check_block(max_rows, E_loc, H, I_loc) != MOE_OK) return 0;
+  if (check_train(max_rows, E_loc, H, I_loc, dt) != MOE_OK) return 0;
   const size_t eb = elt_bytes(dt), rows = max_rows > 0 ? max_rows : 1;
   return align_up(rows * I_loc * eb) + align_up(rows * I_loc * eb * 2) + align_up(rows * H * eb);
 }
@@ -128,8 +138,7 @@ int moe_grouped_ffn_backward(const void* dy_perm, const void* x_perm, const void
                              int max_rows, int H, int I_loc, const void* w13, const void* w2,
                              int dt, const float* gu, void* dx_perm, void* dw13, void* dw2,
                              void* ws, size_t ws_bytes, void* stream) {
-  if (!valid_dt(dt)) return MOE_ERR_INVALID_ARG;
-  const int st = check_block(max_rows, E_loc, H, I_loc);
+  const int st = check_train(max_rows, E_loc, H, I_loc, dt);
   if (st) return st;
   if (!dw13 != !dw2 || (!dx_perm && !dw2)) return MOE_ERR_INVALID_ARG;
   if (any_misaligned(dy_perm, x_perm, x, src_token, offsets, w13, w2, gu, dx_perm, dw13, dw2, ws))
@@ -156,7 +165,7 @@ int moe_grouped_ffn_backward(const void* dy_perm, const void* x_perm, const void
 }
 
 size_t moe_grouped_ffn_mxfp8_workspace_size(int max_rows, int E_loc, int H, int I_loc) {
-  if (check_block(max_rows, E_loc, H, I_loc) != MOE_OK) return 0;
+  if (check_mx(max_rows, E_loc, H, I_loc) != MOE_OK) return 0;
   const size_t rows = max_rows > 0 ? max_rows : 1;
   // h in MXFP8, or in float32 where few rows take that form: the larger of the
   // two for any count up to max_rows, so that a program's largest batch sizes
@@ -173,7 +182,7 @@ int moe_grouped_ffn_mxfp8(const void* x8, const uint8_t* x_scale, const int32_t*
                           const uint8_t* w2_scale, void* y_perm, int y_dt, void* ws,
                           size_t ws_bytes, void* stream) {
   if (!valid_dt(y_dt)) return MOE_ERR_INVALID_ARG;
-  const int st = check_block(max_rows, E_loc, H, I_loc);
+  const int st = check_mx(max_rows, E_loc, H, I_loc);
   if (st) return st;
   if (any_misaligned(x8, x_scale, src_token, offsets, w13, w13_scale, w2, w2_scale, y_perm, ws))
     return MOE_ERR_INVALID_ARG;

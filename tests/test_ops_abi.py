@@ -162,7 +162,7 @@ def test_training_without_rows_needs_nothing_but_the_gradients():
 def test_training_workspaces():
     f, b = M.moe_grouped_ffn_train_workspace_size, M.moe_grouped_ffn_backward_workspace_size
     assert f(65536, 128, 4096, 1536, 1) >= 65536 * 1536 * 2 and b(65536, 128, 4096, 1536, 1) >= 3 * 65536 * 1536 * 2
-    assert f(2 ** 31 - 1, 1, 16384, 65536, 0) > 2 ** 48         # sizes beyond 32 bits
+    assert f(2 ** 22, 8, 4096, 14336, 1) == 2 ** 23 * 14336         # sizes beyond 32 bits
     for q in (f, b):
         for bad in ((-1, 4, 256, 128, 1), (4, 0, 256, 128, 1), (4, 4, 256, 100, 1), (4, 4, 256, 128, 3)):
             assert q(*bad) == 0
@@ -247,3 +247,24 @@ def test_the_binding_runs_on_the_tensors_device(monkeypatch):
     assert seen == [(0, 1000), (1, 1001), (1, 77)] and current[0] == 0
     with pytest.raises(ValueError, match="not cuda:0"):
         ops._call("f", (("a", t0, "f", 4), ("b", t1, "f", 4)), (t0, t1), None)
+
+
+@pytest.mark.parametrize("fn,dt,shapes", [
+    # (max_rows, E_loc, H, I_loc, accepted): the rows' own limit; float32 rows of
+    # outputs; a float32 gradient; the gather of 2^28 rows in bfloat16
+    ("train", 0, [(2 ** 28, 1, 32, 32, True), (2 ** 30 + 1, 1, 32, 32, False), (2 ** 29, 1, 32, 32, False),
+                  (2 ** 26, 1, 32, 256, False), (64, 64, 4096, 16384, True), (64, 128, 4096, 16384, False)]),
+    ("train", 1, [(2 ** 28 - 16, 1, 32, 32, True), (2 ** 28, 1, 32, 32, False), (64, 128, 4096, 16384, True)]),
+    ("mxfp8", None, [(2 ** 30, 1, 32, 32, True), (2 ** 30 + 1, 1, 32, 32, False), (2 ** 30, 1, 32, 2048, False)])])
+def test_shapes_past_a_launch_are_refused(fn, dt, shapes):
+    tail = () if dt is None else (dt,)
+    for rows, E, H, I, good in shapes:
+        assert (getattr(M, f"moe_grouped_ffn_{fn}_workspace_size")(rows, E, H, I, *tail) > 0) == good
+        # with a workspace of one byte an accepted shape stops there, a refused one before
+        want = WORKSPACE if good else UNSUPPORTED
+        if fn == "train":
+            assert (M.moe_grouped_ffn_backward_workspace_size(rows, E, H, I, dt) > 0) == good
+            assert _st("moe_grouped_ffn_train", P, P, P, P, E, rows, H, I, P, P, dt, P, P, P, 1, 0) == want
+            assert _st("moe_grouped_ffn_backward", P, P, P, P, P, E, rows, H, I, P, P, dt, P, P, P, P, P, 1, 0) == want
+        else:
+            assert _st("moe_grouped_ffn_mxfp8", P, P, P, P, E, rows, H, I, P, P, P, P, P, 1, P, 1, 0) == want
