@@ -142,15 +142,18 @@ int moe_grouped_ffn_backward(const void* dy_perm, const void* x_perm, const void
 /*
  * moe_grouped_ffn_mxfp8 -- moe_grouped_ffn on MXFP8 rows and weights.
  *   g, u, y are products of the values the elements and scales stand for,
- *   accumulated in float32 by the scaled matrix instructions; h = SiLU(g) * u
- *   is brought to MXFP8 (blocks of 32 along I_loc) between the two products.
+ *   accumulated in float32; h = SiLU(g) * u is brought to MXFP8 (blocks of 32
+ *   along I_loc) between the two products.  The 8-bit matrix instructions add
+ *   with about 16 significant bits, so an h next to an e4m3 border (one in some
+ *   2000) may round to its other neighbour; with few rows g and u are exact to
+ *   float32.
  *
  *   x8[*][H] with x_scale[*][MOE_MX_PITCH(H)], rows gathered by src_token, or
  *   row r itself when src_token == NULL;
  *   w13[E_loc][2*I_loc][H] with w13_scale[E_loc][2*I_loc][MOE_MX_PITCH(H)];
  *   w2[E_loc][H][I_loc] with w2_scale[E_loc][H][MOE_MX_PITCH(I_loc)];
- *   y_perm[max_rows][H] of dtype y_dt.  Elements must be finite and scale
- *   bytes below 255.  Limits, offsets and sources as for
+ *   y_perm[max_rows][H] of dtype y_dt.  Elements must be finite, scale bytes
+ *   below 255 and the values they stand for below 2^127.  Limits, offsets and sources as for
  *   moe_grouped_ffn_train (a source of -1 gives a meaningless row, which
  *   moe_combine does not read).
  */

@@ -2,13 +2,14 @@
 //
 //   h = MXFP8(SiLU(W_gate a) * (W_up a)),   y = W2 h
 //
-// Both products run on v_mfma_scale_f32_*_f8f6f4, which multiplies e4m3
-// elements and applies one E8M0 scale per 32 of them on either side, so the
-// scales cost no vector instructions: a lane's operand register brings the
-// scale byte of its row's 32-element block.  The instruction sums a block of
-// 64 or 128 products with about 16 significant bits (measured: 1.5e-5 of the
-// result on blocks of normal data, against 2^-4 of an element's own
-// rounding) and accumulates blocks in float32.
+// The products run on v_mfma_scale_f32_*_f8f6f4 (the gate/up product of few
+// rows on bfloat16, below), which multiplies e4m3 elements and applies one E8M0
+// scale per 32 of them on either side, so the scales cost no vector
+// instructions: a lane's operand register brings the scale byte of its row's
+// 32-element block.  The instruction sums a block of 64 or 128 products with
+// about 16 significant bits (measured: 2e-5 of the result on blocks of normal
+// data, against 2^-4 of an element's own rounding) and accumulates blocks in
+// float32.
 //
 // In 32x32x64, lane l holds row l % 32 and, in its two 16-byte halves, the
 // elements 16 (l / 32) + [0, 16) of block 0 and of block 1; the scale of
@@ -340,7 +341,8 @@ __global__ __launch_bounds__(512, 2) void mx_tile_kernel(MxArgs a) {
 
 // ---------------------------------------------------------------------------
 // Direct kernel: 16 rows of one expert against weights streamed from memory
-// into the operands of v_mfma_scale_f32_16x16x128 (weights first, so
+// into the operands of v_mfma_scale_f32_16x16x128, or, in MX_UP, widened to
+// bfloat16 and into those of v_mfma_f32_16x16x32_bf16 (weights first, so
 // accumulator lane l holds columns 4 (l / 16) + i of row l % 16).  A block's 8
 // waves are CW groups of KW = 8 / CW: each group takes its own output columns,
 // and its waves split the contraction and meet in LDS, in wave order.  A wave
@@ -353,7 +355,27 @@ __global__ __launch_bounds__(512, 2) void mx_tile_kernel(MxArgs a) {
 //   MX_DOWN32  the same from float32 h, which the block brings to MXFP8 in LDS
 //              first (the same bits).
 // ---------------------------------------------------------------------------
+// The 8-bit matrix instructions add their products to about 16 bits (2e-5 of a
+// sum measured, whichever form).  That is far below y's own rounding, but moves
+// an h that lies next to an e4m3 border over it, an eighth of its value: about one
+// h in 2000.  In a batch of thousands that is noise (2.0e-3 from the formula,
+// 1.7e-3 with exact sums); in a small one a single h shows.  So the gate/up
+// product of few rows, which waits for memory anyway, runs on bfloat16 values
+// (exact: 4 significant bits, the block's power of two folded in) whose sums are
+// good to 1e-7.
 enum MxMode { MX_UP, MX_DOWN, MX_DOWN32 };
+
+// 8 e4m3 elements times the power of two of scale byte `b`, as bfloat16
+__device__ __forceinline__ bf16x8_t mx_widen(uint32_t lo, uint32_t hi, uint32_t b) {
+  const float s = __uint_as_float(b << 23);      // (only the exponent is read)
+  const bf16x2_v p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, false);
+  const bf16x2_v p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, true);
+  const bf16x2_v p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, false);
+  const bf16x2_v p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, true);
+  const uint4 v = make_uint4(__builtin_bit_cast(uint32_t, p0), __builtin_bit_cast(uint32_t, p1),
+                             __builtin_bit_cast(uint32_t, p2), __builtin_bit_cast(uint32_t, p3));
+  return __builtin_bit_cast(bf16x8_t, v);
+}
 
 __device__ __forceinline__ i32x4_v ld_nt16(const uint8_t* p) {
   return __builtin_nontemporal_load(reinterpret_cast<const i32x4_v*>(p));
@@ -444,10 +466,26 @@ __global__ __launch_bounds__(512, 4) void mx_direct_kernel(MxArgs a) {
         for (int h = 0; h < 2; ++h)
           if (h * 64 + lg * 16 >= left) b.x[u][h] = b.w[u][h] = i32x4_v{0, 0, 0, 0};
       }
+      const uint32_t xs4 = mx_valid_scales(b.xsc[u], left >> 5);
+      const uint32_t ws4 = mx_valid_scales(b.wsc[u], left >> 5);
+      if constexpr (MODE == MX_UP) {
+        // (16 bytes at 64 h + 16 lg: block 2 h + lg / 2)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int sh = 16 * h + 8 * (lg >> 1);
+          const uint32_t xb = (xs4 >> sh) & 0xff, wb = (ws4 >> sh) & 0xff;
+          const i32x4_v x = b.x[u][h], w = b.w[u][h];
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(mx_widen(w[0], w[1], wb),
+                                                        mx_widen(x[0], x[1], xb), acc, 0, 0, 0);
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(mx_widen(w[2], w[3], wb),
+                                                        mx_widen(x[2], x[3], xb), acc, 0, 0, 0);
+        }
+        continue;
+      }
       const i32x8_v xf = __builtin_shufflevector(b.x[u][0], b.x[u][1], 0, 1, 2, 3, 4, 5, 6, 7);
       const i32x8_v wf = __builtin_shufflevector(b.w[u][0], b.w[u][1], 0, 1, 2, 3, 4, 5, 6, 7);
-      const int xsv = (int)((uint32_t)mx_valid_scales(b.xsc[u], left >> 5) >> (8 * lg));
-      const int wsv = (int)((uint32_t)mx_valid_scales(b.wsc[u], left >> 5) >> (8 * lg));
+      const int xsv = (int)(xs4 >> (8 * lg));
+      const int wsv = (int)(ws4 >> (8 * lg));
       acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf, acc, 0, 0, 0, wsv, 0, xsv);
     }
   };
@@ -578,7 +616,8 @@ static hipError_t launch_mx_direct_t(const MxArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 // Which kernel takes each product.  Measured on MI355X, replayed from a graph
-// (us; up kernel / down kernel; d<n>: direct with n column groups per block):
+// (us; up kernel / down kernel; d<n>: direct with n column groups per block; the
+// direct gate/up products on bfloat16 take 1-3% more of the whole):
 //   I/P = 192, 8 experts x 1 row:     d1/d8 11.4  d2/d8 13.7  d4/d8 20.1  tiles 40.2
 //     49 experts:                     d1/d8 42.4  d2/d8 44.8  tiles 59.2
 //     87 experts:                     d1/d8 69.9  tiles/d8 64.4  tiles 74.8
@@ -588,6 +627,13 @@ static hipError_t launch_mx_direct_t(const MxArgs& a, hipStream_t st) {
 //     13 experts:                     d2/d8 155   tiles 138
 //   I = 14336, 2 experts:             tiles/d2 74.3  tiles/d8 147  d4/d8 173  tiles 207
 //     8 experts, 4 rows each:         tiles/d2 345   tiles 367
+//   many rows per expert (direct / tiles; outputs as row tiles of 16 x I / 8):
+//     248:  936 rows, 4 experts, I 32, H 2976     18.3 / 52.4
+//     256:  1024 rows, 1 expert, I 32, H 768      9.8 / 23.0
+//     1260: 330 rows, 1 expert, I 480, H 192      17.3 / 23.1
+//     1728: 1024 rows, 8 experts, I 192, H 4096   64.2 / 64.5
+//     2568: 1710 rows, 1 expert, I 192, H 128     25.4 / 17.8
+//     5280: 7016 rows, 4 experts, I 96, H 1312    92.7 / 33.7
 // The tiled kernel streams faster (5.1 against 4.1 TB/s) but needs a block of
 // 1 MB of weights per CU; a contraction of one or two steps gains nothing from
 // its pipeline; and the direct kernel's 16-row tiles read the weights again
@@ -604,7 +650,9 @@ static MxPlan mx_plan(int max_rows, int E, int H, int I) {
   // experts with rows, were every row's expert drawn alike, and their row tiles
   const double touched = E * (1.0 - __builtin_pow(1.0 - 1.0 / E, (double)max_rows));
   const double tiles = std::max(touched, max_rows / 128.0);
-  const bool few = mean <= 64;
+  // few rows per expert, or so few outputs of the gate/up product that 8-column
+  // blocks of 16 rows do not fill the CUs
+  const bool few = mean <= 64 || (max_rows / 16 + touched) * (I / 8) <= 1536;
   p.up_direct = few && tiles * ((I + 127) / 128) < MX_MIN_BLOCKS;
   p.down_direct = few && (I <= 256 || tiles * ((H + 255) / 256) < 256);
   const int steps = (I + 127) / 128;

@@ -204,6 +204,14 @@ def test_graph_replays():
 # (columns in groups of 32, contraction split over 2 and 4 waves), h in float32
 # from groups of 8 and 16 columns, direct up with tiled down, tiled up with
 # direct down
+# more than 64 rows per expert, and few outputs: 16-row blocks all the same
+@pytest.mark.parametrize("counts,H,I", [([300, 0, 129], 1376, 32), ([1030], 96, 64), ([65], 4096, 192), ([300], 160, 480)])
+def test_many_rows_and_few_columns(counts, H, I):
+    b = Block(counts, H, I, seed=28, spread=True)
+    for y_dt in (BF16, F32):
+        b.verify(b.run(y_dt))
+
+
 @pytest.mark.parametrize("counts,H,I", [
     ([1, 0, 3], 64, 2080), ([2, 1], 96, 6240), ([8] * 9, 256, 1056), ([1, 2], 4096, 192),
     ([1, 2, 0, 1] * 18, 1376, 288), ([2, 1, 3] * 32, 160, 224), ([70], 256, 128), ([33, 50], 288, 2112)])
