@@ -20,6 +20,11 @@
 // Few rows per expert: the weights are the traffic, and the direct kernel
 // streams them from memory into the operands.  Many rows: the tiled kernel,
 // operands staged through LDS.
+//
+// Measured on MI355X, Qwen3 shape (128 experts, H 4096, I 1536): T = 64 462 us,
+// 5.3 TB/s of weights (a large copy: 5.1); T = 8192 gate/up 1.10 ms and down 0.61,
+// 1.4-1.5 PFLOP/s, bound by operand loads beyond L2 (matrix cores busy 0.36-0.39).
+// One token of an eighth of it (I 192): 11 us in two launches, latency.
 #include <algorithm>
 #include <type_traits>
 

@@ -24,6 +24,12 @@
 //     activation is ever written.
 //
 // Both reach LDS by 16-byte direct loads (1 KB per wave instruction).
+//
+// Measured on MI355X.  Mixtral shape, 8 experts, T = 4096 (R = 8192 rows): gate/up
+// 1.98 ms, down 0.95, dh 1.20, dx 1.84, both weight gradients 3.04: 0.80 to 1.05
+// PFLOP/s, matrix cores busy 0.50-0.54 at 1.85-1.95 GHz (dh 0.40: its epilogue
+// moves 1.6 GB).  Qwen3 shape, 128 experts, 32 rows each: bound by the weights and
+// their gradients, 14.5 GB in 2.65 ms.
 #include <algorithm>
 #include <type_traits>
 
@@ -571,9 +577,12 @@ __global__ __launch_bounds__(512, 2) void train_rows_kernel(GemmArgs a) {
   RowBlock t;
   if (!row_block<GEMM_TM>(a.offsets, a.E, a.max_rows, NT, blockIdx.x, t)) return;
   const int r0 = t.r0, r1 = t.r1, n0 = t.n * COLS;
-  if (r1 - r0 > 128) gemm_tile<GemmT256, false, BKC, EPI, GATHER>(a, smem, t.e, r0, r1, n0, a.K, 0);
-  else if (r1 - r0 > 64) gemm_tile<GemmT128, false, BKC, EPI, GATHER>(a, smem, t.e, r0, r1, n0, a.K, 0);
-  else gemm_tile<GemmT64, false, BKC, EPI, GATHER>(a, smem, t.e, r0, r1, n0, a.K, 0);
+  if (r1 - r0 > 128)
+    gemm_tile<GemmT256, false, BKC, EPI, GATHER>(a, smem, t.e, r0, r1, n0, a.K, 0);
+  else if (r1 - r0 > 64)
+    gemm_tile<GemmT128, false, BKC, EPI, GATHER>(a, smem, t.e, r0, r1, n0, a.K, 0);
+  else
+    gemm_tile<GemmT64, false, BKC, EPI, GATHER>(a, smem, t.e, r0, r1, n0, a.K, 0);
 }
 
 // Weight gradients: contractions as long as an expert has rows, often a few
@@ -635,9 +644,11 @@ __global__ __launch_bounds__(256) void train_gather_kernel(const uint4* x, const
 // block takes 32 x 32 outputs and its 4 waves split the contraction in
 // interleaved chunks of 16, each with the next chunk's loads in flight; they
 // meet in LDS in wave order.  (WAVES: a wave takes 32 x 32 outputs of a weight
-// gradient alone, where a few rows per expert leave nothing to split.)  A lane's four elements of a chunk feed four
-// products: element i of lane l stands for k = 4 (l / 16) + i in both operands.
-// (64 x 64 tiles of plain multiply-adds: 343 us for the toy layer's step.)
+// gradient alone, where a few rows per expert leave nothing to split.)  A lane's
+// four elements of a chunk feed four products: element i of lane l stands for
+// k = 4 (l / 16) + i in both operands.  The toy layer's step takes 34 us, four
+// dependent launches bound by their chains of loads (64 x 64 tiles of plain
+// multiply-adds: 343 us); three to six chunks in flight took 36 to 45.
 // ---------------------------------------------------------------------------
 struct F32GemmArgs {
   const float* A;
@@ -730,7 +741,8 @@ __device__ __forceinline__ void f32_tile(const F32GemmArgs& a, int block, float*
 #pragma unroll
     for (int i = 0; i < 2; ++i) c.a[i] = WGRAD ? across(ap[i], a.lda, k, nullptr) : along(ap[i], k);
 #pragma unroll
-    for (int i = 0; i < NB; ++i) c.b[i] = BKC ? along(bp[i], k) : across(bp[i], a.ldb, k, WGRAD ? a.src_token : nullptr);
+    for (int i = 0; i < NB; ++i)
+      c.b[i] = BKC ? along(bp[i], k) : across(bp[i], a.ldb, k, WGRAD ? a.src_token : nullptr);
   };
   f32x4_t acc[2][NB];
 #pragma unroll
@@ -765,8 +777,8 @@ __device__ __forceinline__ void f32_tile(const F32GemmArgs& a, int block, float*
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int j = 0; j < NB; ++j)
-        *reinterpret_cast<float4*>(out + (size_t)(r0 + 16 * i + lr) * a.ldo + n0 + 16 * j + 4 * lg) =
-            make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
+        *reinterpret_cast<float4*>(out + (size_t)(r0 + 16 * i + lr) * a.ldo + n0 + 16 * j +
+                                   4 * lg) = make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
     return;
   }
 #pragma unroll
