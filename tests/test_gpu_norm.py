@@ -87,6 +87,23 @@ def test_norm(T, H, dt, residual):
     check_mx(o["y8"], o["scale"], y, STAT + 3 * U)
 
 
+@pytest.mark.parametrize("dt", TYPES)
+def test_norm_rounds_once_to_8_bits(dt):
+    """Every element of 2^24 is the e4m3 value nearest to the formula's float64
+    value: both are within 2^-51 of the real one, so that an element lies between
+    them and a border 2^-4 apart in about one case of 2^46."""
+    T, H, eps = 4096, 4096, 2.0 ** -20
+    x, res, w = _rand((T, H), 51, 1.5, dt), _rand((T, H), 52, 1.0, dt), (1 + _rand((H,), 53, 0.1)).to(dt)
+    o = _norm(x, res, w, eps=eps)
+    ref = _reference(x, res, w, eps)[2].reshape(T, H // 32, 32)
+    k = torch.exp2(o["scale"].double() - 127)[:, :, None]
+    a = (ref / k).abs()
+    step = torch.exp2(torch.floor(torch.log2(a.clamp_min(2.0 ** -6))) - 3)       # 3 mantissa bits, least step 2^-9
+    want = torch.round(a / step) * step * torch.sign(ref)
+    assert (a.amax(-1) <= 448).all() and (a.amax(-1) > 224).all()
+    assert torch.equal(o["y8"].double().reshape(want.shape), want)
+
+
 @pytest.mark.parametrize("want", ["sum", "y", "y8", "rstd"])
 def test_norm_outputs_alone_equal_those_together(want):
     x, res, w = _rand((9, 4096), 4, 1.0, torch.bfloat16), _rand((9, 4096), 5, 1.0, torch.bfloat16), _rand((4096,), 6, 1.0, torch.bfloat16)
