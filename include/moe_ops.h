@@ -40,6 +40,9 @@ extern "C" {
 
 /* Scale bytes of an MXFP8 row of K elements. */
 #define MOE_MX_PITCH(K) (((K) + 127) / 128 * 4)
+/* Added to dt = MOE_BF16: the gate and up projections that a training block
+ * saves are bfloat16 as well, not float32. */
+#define MOE_GU_BF16 0x100
 
 /*
  * moe_rmsnorm -- the norm between the residual stream and the layer.
@@ -100,16 +103,20 @@ int moe_combine_backward(const void* dy, int dt, const void* y_perm, int y_perm_
  *   For expert i and every row r in [offsets[i], offsets[i+1]), with
  *   a = x_perm[r], or x[src_token[r]] when x_perm == NULL:
  *     forward   g = W_gate a, u = W_up a, h = SiLU(g) * u, y_perm[r] = W2 h,
- *               gu[r] = [g | u]  (float32, [max_rows][2*I_loc])
+ *               gu[r] = [g | u]  ([max_rows][2*I_loc])
  *     backward  dh = W2^T dy_perm[r]
  *               dg = dh * u * SiLU'(g), du = dh * SiLU(g),
  *               SiLU'(g) = s (1 + g (1 - s)), s = 1 / (1 + exp(-g))
  *               dx_perm[r] = W_gate^T dg + W_up^T du
  *               dw13[i] = sum_r [dg | du] a^T,  dw2[i] = sum_r dy_perm[r] h^T
- *   The backward pass reads g and u from gu and forms h anew.  h, dg and du
- *   are rounded to dt before the products that read them, as h is in the
- *   forward pass; g and u are kept unrounded, so a gradient passes one
- *   rounding between its two products, as the output does.
+ *   gu is float32, or bfloat16 with dt = MOE_BF16 | MOE_GU_BF16 in both calls
+ *   (the Python binding goes by gu's own type).  The backward pass reads g and u
+ *   from gu and forms h anew.  h, dg and du are rounded to dt before the
+ *   products that read them, as h is in the forward pass.  A float32 gu holds g
+ *   and u unrounded, so a gradient passes one rounding between its two products,
+ *   as the output does; a bfloat16 gu takes half the memory and adds the
+ *   rounding of g and u (against float64, in 2-norm: dx_perm, dw13 and dw2
+ *   2.3e-3 with float32; 3.0e-3, 3.0e-3 and 3.5e-3 with bfloat16).
  *
  *   dy_perm, dx_perm, y_perm: [max_rows][H]; dw13, dw2: shapes of w13, w2; all
  *   dtype dt.  dx_perm may be NULL, and dw13 and dw2 together may be NULL (not
@@ -130,13 +137,13 @@ int moe_combine_backward(const void* dy, int dt, const void* y_perm, int y_perm_
 size_t moe_grouped_ffn_train_workspace_size(int max_rows, int E_loc, int H, int I_loc, int dt);
 int moe_grouped_ffn_train(const void* x_perm, const void* x, const int32_t* src_token,
                           const int32_t* offsets, int E_loc, int max_rows, int H, int I_loc,
-                          const void* w13, const void* w2, int dt, float* gu, void* y_perm,
+                          const void* w13, const void* w2, int dt, void* gu, void* y_perm,
                           void* ws, size_t ws_bytes, void* stream);
 size_t moe_grouped_ffn_backward_workspace_size(int max_rows, int E_loc, int H, int I_loc, int dt);
 int moe_grouped_ffn_backward(const void* dy_perm, const void* x_perm, const void* x,
                              const int32_t* src_token, const int32_t* offsets, int E_loc,
                              int max_rows, int H, int I_loc, const void* w13, const void* w2,
-                             int dt, const float* gu, void* dx_perm, void* dw13, void* dw2,
+                             int dt, const void* gu, void* dx_perm, void* dw13, void* dw2,
                              void* ws, size_t ws_bytes, void* stream);
 
 /*

@@ -65,7 +65,8 @@ struct GemmArgs {
   long long ldo;
   long long out_stride;       // elements between experts' outputs (weight gradients)
   bf16_t* out2;               // EPI_SWIGLU, EPI_DSWIGLU: h [rows][N]
-  float* gu;                  // [rows][2 N] of EPI_SWIGLU (written) and EPI_DSWIGLU (read)
+  void* gu;                   // [rows][2 N] of EPI_SWIGLU (written) and EPI_DSWIGLU (read)
+  bool gu_bf16;               // its type, else float32
 };
 
 // Tile shape: TM x TN outputs, STAGES buffers of 64 along the contraction,
@@ -137,6 +138,17 @@ __device__ __forceinline__ void tr_read(const uint32_t (&at)[4], bf16x8_t (&f)[4
   f[1] = tr_join(b0, b1);
   f[2] = tr_join(c0, c1);
   f[3] = tr_join(d0, d1);
+}
+
+// Four consecutive elements, aligned to them.
+__device__ __forceinline__ void load4(const float* p, float (&f)[4]) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+}
+__device__ __forceinline__ void load4(const bf16_t* p, float (&f)[4]) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  f[0] = __uint_as_float(v.x << 16); f[1] = __uint_as_float(v.x & 0xffff0000u);
+  f[2] = __uint_as_float(v.y << 16); f[3] = __uint_as_float(v.y & 0xffff0000u);
 }
 
 // One output tile: rows [r0, r1) (of expert e; in a weight gradient, rows of the
@@ -457,24 +469,48 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, unsigned char* smem
     store(out, a.ldo);
   }
   if constexpr (EPI == EPI_SWIGLU) {
-    // g, u (TN / 2 columns of float32 fill a staged row of TN bfloat16), then h
+    // g, u (TN / 2 columns of float32 fill a staged row of TN bfloat16; in
+    // bfloat16 both fit side by side), then h
     constexpr int HALF = C::MFN / 2;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
+    if (a.gu_bf16) {
 #pragma unroll
       for (int mi = 0; mi < C::MFM; ++mi)
 #pragma unroll
-        for (int ni = 0; ni < HALF; ++ni)
+        for (int ni = 0; ni < C::MFN; ++ni)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const f32x16_t& v = acc[mi][ni + half * HALF];
-            *reinterpret_cast<float4*>(smem + (wm * C::WTM + mi * 32 + lrow) * C::PITCH +
-                                       (nbase[ni] + 8 * q + 4 * khalf) * 4) =
-                make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-          }
+          for (int q = 0; q < 4; ++q)
+            put(mi, nbase[ni] + 8 * q + 4 * khalf,
+                cvt_bf16x2(acc[mi][ni][4 * q], acc[mi][ni][4 * q + 1]),
+                cvt_bf16x2(acc[mi][ni][4 * q + 2], acc[mi][ni][4 * q + 3]));
       lds_barrier();
-      store(a.gu + half * a.up_off, 2LL * a.N);
+      constexpr int CPR = COLS / 8;
+      for (int c = threadIdx.x; c < C::TM * 2 * CPR; c += C::NTHR) {
+        const int r = c / (2 * CPR), cc = c - r * (2 * CPR), half = cc / CPR;
+        const int col = n0 + (cc - half * CPR) * 8;
+        if (r < nrows && col < a.N)
+          st_nt16(static_cast<bf16_t*>(a.gu) + (size_t)(r0 + r) * (2 * (size_t)a.N) +
+                      half * a.up_off + col,
+                  *reinterpret_cast<const uint4*>(smem + r * C::PITCH + cc * 16));
+      }
       lds_barrier();
+    } else {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int mi = 0; mi < C::MFM; ++mi)
+#pragma unroll
+          for (int ni = 0; ni < HALF; ++ni)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const f32x16_t& v = acc[mi][ni + half * HALF];
+              *reinterpret_cast<float4*>(smem + (wm * C::WTM + mi * 32 + lrow) * C::PITCH +
+                                         (nbase[ni] + 8 * q + 4 * khalf) * 4) =
+                  make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            }
+        lds_barrier();
+        store(static_cast<float*>(a.gu) + half * a.up_off, 2LL * a.N);
+        lds_barrier();
+      }
     }
 #pragma unroll
     for (int mi = 0; mi < C::MFM; ++mi)
@@ -499,62 +535,65 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, unsigned char* smem
     constexpr int RB = C::WM * 32, REGION = RB * C::PITCH;
     constexpr bool THREE = 3 * REGION <= C::LDS;
     static_assert(2 * REGION <= C::LDS, "staged rows");
+    auto rows = [&](const auto* gu) {
 #pragma unroll
-    for (int mi = 0; mi < C::MFM; ++mi) {
-      const int row = min(r0 + wm * C::WTM + mi * 32 + lrow, r1 - 1);
-      const float* gr = a.gu + (size_t)row * (2 * (size_t)a.N);
-      unsigned char* so = smem + (wm * 32 + lrow) * C::PITCH;
-      uint2 hp[C::MFN][4];
+      for (int mi = 0; mi < C::MFM; ++mi) {
+        const int row = min(r0 + wm * C::WTM + mi * 32 + lrow, r1 - 1);
+        const auto* gr = gu + (size_t)row * (2 * (size_t)a.N);
+        unsigned char* so = smem + (wm * 32 + lrow) * C::PITCH;
+        uint2 hp[C::MFN][4];
 #pragma unroll
-      for (int ni = 0; ni < C::MFN; ++ni) {
-        const int col = n0 + nbase[ni] < a.N ? n0 + nbase[ni] : 0;   // whole 32s in or out
+        for (int ni = 0; ni < C::MFN; ++ni) {
+          const int col = n0 + nbase[ni] < a.N ? n0 + nbase[ni] : 0;   // whole 32s in or out
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int c = col + 8 * q + 4 * khalf;
-          const float4 g4 = *reinterpret_cast<const float4*>(gr + c);
-          const float4 u4 = *reinterpret_cast<const float4*>(gr + a.N + c);
-          const float g[4] = {g4.x, g4.y, g4.z, g4.w}, u[4] = {u4.x, u4.y, u4.z, u4.w};
-          float dg[4], du[4], h[4];
+          for (int q = 0; q < 4; ++q) {
+            const int c = col + 8 * q + 4 * khalf;
+            float g[4], u[4], dg[4], du[4], h[4];
+            load4(gr + c, g);
+            load4(gr + a.N + c, u);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float dh = acc[mi][ni][4 * q + r];
-            const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-g[r])), sg = g[r] * s;
-            h[r] = sg * u[r];
-            dg[r] = dh * u[r] * (s + sg * (1.0f - s));
-            du[r] = dh * sg;
+            for (int r = 0; r < 4; ++r) {
+              const float dh = acc[mi][ni][4 * q + r];
+              const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-g[r])), sg = g[r] * s;
+              h[r] = sg * u[r];
+              dg[r] = dh * u[r] * (s + sg * (1.0f - s));
+              du[r] = dh * sg;
+            }
+            uint2* p = reinterpret_cast<uint2*>(so + (nbase[ni] + 8 * q + 4 * khalf) * 2);
+            p[0] = make_uint2(cvt_bf16x2(dg[0], dg[1]), cvt_bf16x2(dg[2], dg[3]));
+            p[REGION / 8] = make_uint2(cvt_bf16x2(du[0], du[1]), cvt_bf16x2(du[2], du[3]));
+            hp[ni][q] = make_uint2(cvt_bf16x2(h[0], h[1]), cvt_bf16x2(h[2], h[3]));
+            if (THREE) p[2 * REGION / 8] = hp[ni][q];
           }
-          uint2* p = reinterpret_cast<uint2*>(so + (nbase[ni] + 8 * q + 4 * khalf) * 2);
-          p[0] = make_uint2(cvt_bf16x2(dg[0], dg[1]), cvt_bf16x2(dg[2], dg[3]));
-          p[REGION / 8] = make_uint2(cvt_bf16x2(du[0], du[1]), cvt_bf16x2(du[2], du[3]));
-          hp[ni][q] = make_uint2(cvt_bf16x2(h[0], h[1]), cvt_bf16x2(h[2], h[3]));
-          if (THREE) p[2 * REGION / 8] = hp[ni][q];
         }
-      }
-      auto leave = [&](bf16_t* y, long long ld, int region) {
-        constexpr int CPR = C::TN / 8;
-        for (int c = threadIdx.x; c < RB * CPR; c += C::NTHR) {
-          const int r = c / CPR, cc = c - r * CPR, col = n0 + cc * 8;
-          const int rt = (r >> 5) * C::WTM + mi * 32 + (r & 31);     // row of the tile
-          if (rt < nrows && col < a.N)
-            st_nt16(y + (size_t)(r0 + rt) * ld + col,
-                    *reinterpret_cast<const uint4*>(smem + region + r * C::PITCH + cc * 16));
-        }
-      };
-      lds_barrier();
-      leave(out, a.ldo, 0);
-      leave(out + a.up_off, a.ldo, REGION);
-      if constexpr (!THREE) {
+        auto leave = [&](bf16_t* y, long long ld, int region) {
+          constexpr int CPR = C::TN / 8;
+          for (int c = threadIdx.x; c < RB * CPR; c += C::NTHR) {
+            const int r = c / CPR, cc = c - r * CPR, col = n0 + cc * 8;
+            const int rt = (r >> 5) * C::WTM + mi * 32 + (r & 31);     // row of the tile
+            if (rt < nrows && col < a.N)
+              st_nt16(y + (size_t)(r0 + rt) * ld + col,
+                      *reinterpret_cast<const uint4*>(smem + region + r * C::PITCH + cc * 16));
+          }
+        };
         lds_barrier();
+        leave(out, a.ldo, 0);
+        leave(out + a.up_off, a.ldo, REGION);
+        if constexpr (!THREE) {
+          lds_barrier();
 #pragma unroll
-        for (int ni = 0; ni < C::MFN; ++ni)
+          for (int ni = 0; ni < C::MFN; ++ni)
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<uint2*>(so + (nbase[ni] + 8 * q + 4 * khalf) * 2) = hp[ni][q];
+            for (int q = 0; q < 4; ++q)
+              *reinterpret_cast<uint2*>(so + (nbase[ni] + 8 * q + 4 * khalf) * 2) = hp[ni][q];
+          lds_barrier();
+        }
+        leave(a.out2, a.N, THREE ? 2 * REGION : 0);
         lds_barrier();
       }
-      leave(a.out2, a.N, THREE ? 2 * REGION : 0);
-      lds_barrier();
-    }
+    };
+    if (a.gu_bf16) rows(static_cast<const bf16_t*>(a.gu));
+    else rows(static_cast<const float*>(a.gu));
   }
 }
 
@@ -917,12 +956,13 @@ struct Product {
 static GemmArgs bf16_args(const TrainFfn& f, const Product& p) {
   return GemmArgs{(const bf16_t*)p.A, (const bf16_t*)p.B, p.lda, p.ldb, p.b_stride, p.src,
                   f.offsets, f.E, f.max_rows, p.M, p.N, p.K, p.up_off, (bf16_t*)p.out, p.ldo,
-                  p.out_stride, (bf16_t*)p.out2, f.gu};
+                  p.out_stride, (bf16_t*)p.out2, f.gu, f.gu_bf16};
 }
 static F32GemmArgs f32_args(const TrainFfn& f, const Product& p) {
   return F32GemmArgs{(const float*)p.A, (const float*)p.B, p.lda, p.ldb, p.b_stride, p.src,
                      f.offsets, f.E, f.max_rows, p.M, p.N, p.K, p.up_off, (float*)p.out, p.ldo,
-                     p.out_stride, (float*)p.out2, f.gu};
+                     p.out_stride, (float*)p.out2,
+                     static_cast<const float*>(f.gu)};
 }
 template <bool BKC, int EPI>
 static hipError_t rows_product(const TrainFfn& f, const Product& p, hipStream_t st) {

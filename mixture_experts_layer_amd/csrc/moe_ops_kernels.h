@@ -36,7 +36,8 @@ struct TrainFfn {
   int E, max_rows, H, I, dt;
   const void* w13;
   const void* w2;
-  float* gu;                // [max_rows][2 I]: written by the forward pass, read by the backward
+  void* gu;                 // [max_rows][2 I]: written by the forward pass, read by the backward
+  bool gu_bf16;             // its type (bfloat16 rows; else float32)
   void* h;                  // [max_rows][I], workspace
 };
 constexpr int OPS_MAX_DIM = 65536;               // H and I of the expert blocks

@@ -9,7 +9,8 @@ streams.
 """
 from __future__ import annotations
 
-from ._abi import MOE_BF16, MOE_F32
+from ._abi import MOE_BF16, MOE_F32, MOE_GU_BF16
+
 
 def mx_pitch(K: int) -> int:
     """Scale bytes of an MXFP8 row of K elements (MOE_MX_PITCH)."""
@@ -73,6 +74,17 @@ def _launch(fn, argv, dev, stream):
     return getattr(_LIB, fn)(*argv, stream)
 
 
+def _gu(gu, dt):
+    """dt of a training block's rows, its gu's type for _call, and dt as the
+    library takes it: bfloat16 rows may save gu in either type."""
+    dt &= ~MOE_GU_BF16
+    if _LIB is None:
+        _setup()
+    if dt == MOE_BF16 and gu is not None and gu.dtype == _TYPES[MOE_BF16][0]:
+        return dt, MOE_BF16, dt | MOE_GU_BF16
+    return dt, "f", dt
+
+
 def moe_rmsnorm(x, residual, weight, eps, T, H, dt, sum, y, y8, y8_scale, rstd, stream=None):
     n = T * H
     _call("moe_rmsnorm",
@@ -114,14 +126,15 @@ def moe_grouped_ffn_train_workspace_size(max_rows, E_loc, H, I_loc, dt) -> int:
 def moe_grouped_ffn_train(x_perm, x, src_token, offsets, E_loc, max_rows, H, I_loc, w13, w2, dt, gu,
                           y_perm, ws, ws_bytes, stream=None):
     n = max_rows * H
+    dt, kind, flagged = _gu(gu, dt)
     _call("moe_grouped_ffn_train",
           (("x_perm", x_perm, dt, n), ("x", x, dt, 0),
            ("src_token", src_token, "i", 0 if x_perm is not None else max_rows),
            ("offsets", offsets, "i", E_loc + 1), ("w13", w13, dt, 2 * E_loc * I_loc * H),
-           ("w2", w2, dt, E_loc * I_loc * H), ("gu", gu, "f", 2 * max_rows * I_loc),
+           ("w2", w2, dt, E_loc * I_loc * H), ("gu", gu, kind, 2 * max_rows * I_loc),
            ("y_perm", y_perm, dt, n), ("ws", ws, "b", ws_bytes)),
-          (x_perm, x, src_token, offsets, E_loc, max_rows, H, I_loc, w13, w2, dt, gu, y_perm, ws,
-           ws_bytes), stream)
+          (x_perm, x, src_token, offsets, E_loc, max_rows, H, I_loc, w13, w2, flagged, gu, y_perm,
+           ws, ws_bytes), stream)
 
 
 def moe_grouped_ffn_backward_workspace_size(max_rows, E_loc, H, I_loc, dt) -> int:
@@ -132,15 +145,16 @@ def moe_grouped_ffn_backward_workspace_size(max_rows, E_loc, H, I_loc, dt) -> in
 def moe_grouped_ffn_backward(dy_perm, x_perm, x, src_token, offsets, E_loc, max_rows, H, I_loc, w13,
                              w2, dt, gu, dx_perm, dw13, dw2, ws, ws_bytes, stream=None):
     n, weights = max_rows * H, E_loc * I_loc * H
+    dt, kind, flagged = _gu(gu, dt)
     _call("moe_grouped_ffn_backward",
           (("dy_perm", dy_perm, dt, n), ("x_perm", x_perm, dt, n), ("x", x, dt, 0),
            ("src_token", src_token, "i", 0 if x_perm is not None else max_rows),
            ("offsets", offsets, "i", E_loc + 1), ("w13", w13, dt, 2 * weights),
-           ("w2", w2, dt, weights), ("gu", gu, "f", 2 * max_rows * I_loc),
+           ("w2", w2, dt, weights), ("gu", gu, kind, 2 * max_rows * I_loc),
            ("dx_perm", dx_perm, dt, n), ("dw13", dw13, dt, 2 * weights),
            ("dw2", dw2, dt, weights), ("ws", ws, "b", ws_bytes)),
-          (dy_perm, x_perm, x, src_token, offsets, E_loc, max_rows, H, I_loc, w13, w2, dt, gu,
-           dx_perm, dw13, dw2, ws, ws_bytes), stream)
+          (dy_perm, x_perm, x, src_token, offsets, E_loc, max_rows, H, I_loc, w13, w2, flagged,
+           gu, dx_perm, dw13, dw2, ws, ws_bytes), stream)
 
 
 def moe_grouped_ffn_mxfp8_workspace_size(max_rows, E_loc, H, I_loc) -> int:

@@ -268,3 +268,55 @@ def test_shapes_past_a_launch_are_refused(fn, dt, shapes):
             assert _st("moe_grouped_ffn_backward", P, P, P, P, P, E, rows, H, I, P, P, dt, P, P, P, P, P, 1, 0) == want
         else:
             assert _st("moe_grouped_ffn_mxfp8", P, P, P, P, E, rows, H, I, P, P, P, P, P, 1, P, 1, 0) == want
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The binding's calls with tensors that say they live on GPU 0: [(function,
+    arguments as the library would get them)]."""
+    from contextlib import nullcontext
+    from types import SimpleNamespace
+
+    from mixture_experts_layer_amd import ops
+    seen = []
+    ops._setup()
+    monkeypatch.setattr(ops, "_TORCH", SimpleNamespace(Tensor=torch.Tensor, cuda=SimpleNamespace(
+        current_device=lambda: 0, device=lambda d: nullcontext())))
+    monkeypatch.setattr(ops, "_launch", lambda fn, argv, dev, stream: seen.append((fn, argv)) or 0)
+    return seen
+
+
+def _gpu(*shape, dt=torch.bfloat16):
+    return _OnDevice(torch.zeros(shape, dtype=dt), 0)
+
+
+def test_the_saved_projections_may_be_of_the_rows_type(calls):
+    """gu of a bfloat16 block is float32 or bfloat16, as the caller has it; the
+    C entries read which from dt, and the binding from the tensor."""
+    b, f, i = torch.bfloat16, torch.float32, torch.int32
+    z = _gpu
+
+    def train(t, gu, dt):
+        M.moe_grouped_ffn_train(None, z(4, 64, dt=t), z(4, dt=i), z(3, dt=i), 2, 4, 64, 32, z(2, 64, 64, dt=t),
+                                z(2, 64, 32, dt=t), dt, gu, z(4, 64, dt=t), z(64, dt=torch.uint8), 64)
+
+    def backward(t, gu, dt):
+        M.moe_grouped_ffn_backward(z(4, 64, dt=t), None, z(4, 64, dt=t), z(4, dt=i), z(3, dt=i), 2, 4, 64, 32,
+                                   z(2, 64, 64, dt=t), z(2, 64, 32, dt=t), dt, gu, z(4, 64, dt=t), None, None,
+                                   z(64, dt=torch.uint8), 64)
+    flag = int(re.search(r"#define MOE_GU_BF16 (\w+)", open(HEADER).read()).group(1), 0)
+    for call, at in ((train, 10), (backward, 11)):
+        for t, gu, dt, want in ((b, z(4, 64), 1, 1 | flag), (b, z(4, 64, dt=f), 1, 1), (f, z(4, 64, dt=f), 0, 0)):
+            call(t, gu, dt)
+            assert calls.pop()[1][at] == want
+        for t, gu, dt in ((f, z(4, 64), 0), (b, z(4, 64, dt=torch.float16), 1)):
+            with pytest.raises(TypeError, match="gu is"):
+                call(t, gu, dt)
+        with pytest.raises(ValueError, match="gu holds 192 elements"):
+            call(b, z(3, 64), 1)
+    for fn, a in (("moe_grouped_ffn_train", TRAIN), ("moe_grouped_ffn_backward", BACKWARD)):
+        assert _st(fn, *dict(a, dt=1 | flag, ws_bytes=1).values()) == WORKSPACE
+        assert _st(fn, *dict(a, dt=0 | flag).values()) == INVALID
+        assert _st(fn, *dict(a, dt=2 | flag).values()) == INVALID
+        q = getattr(M, fn + "_workspace_size")
+        assert q(16, 4, 256, 128, 1 | flag) == q(16, 4, 256, 128, 1) > 0 == q(16, 4, 256, 128, flag)
