@@ -207,7 +207,7 @@ def prepare(case, seed):
         return s
     s.update(x=_randn(g, (T, H), 1.0, dt), dy=_randn(g, (R, H), 0.02, dt),
              w13=_experts(g, E, (2 * I, H), s["scale"], dt), w2=_experts(g, E, (H, I), s["scale"], dt),
-             gu=e(R, 2 * I, dtype=torch.float32), y=e(R, H), dx=e(R, H), dw13=e(E, 2 * I, H), dw2=e(E, H, I))
+             gu=e(R, 2 * I), y=e(R, H), dx=e(R, H), dw13=e(E, 2 * I, H), dw2=e(E, H, I))
     return s
 
 
