@@ -29,10 +29,10 @@ struct NormArgs {
   int H, n_chunk, pitch;
 };
 
-// The statistic and the products that an e4m3 element is rounded from are taken
-// in float64: the memory's time hides them, no row's squares overflow, and an
-// element next to a rounding border falls on the side that the formula says,
-// whatever the order of the sum.
+// The statistic and the products are taken in float64: the memory's time hides
+// them, neither a row's squares nor s * w, whose product with rstd may be an
+// ordinary number again, leave the range, and an element next to a rounding
+// border falls on the side that the formula says, whatever the order of the sum.
 //
 // On the way to 8 bits and to bfloat16 a value passes float32 rounded to odd
 // (a last bit of 1 stands for "and a little more"), so that it is rounded once:
@@ -96,8 +96,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs a) {
       w[i].get(q);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const double p = (BF16 ? (double)(f[e] * q[e])      // exact: 8 by 8 significant bits
-                               : (double)f[e] * (double)q[e]) * rstd;
+        const double p = (double)f[e] * (double)q[e] * rstd;   // (the first product is exact)
         f[e] = to_odd_f32(p);
         y[e] = BF16 ? f[e] : (float)p;
       }

@@ -133,6 +133,20 @@ def test_norm_extremes_and_blocks_at_the_scale_border():
     assert torch.isfinite(o["y"][2:]).all()
 
 
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("rows,weight,eps", [(2.0 ** 126, 4.0, 1e-6), (2.0 ** -100, 2.0 ** -45, 0.0), (2.0 ** -120, 2.0 ** -20, 0.0),
+                                             (2.0 ** 100, 2.0 ** 100, 1e-6)])
+def test_norm_products_outside_float32(dt, rows, weight, eps):
+    """s * weight may leave float32's range where s * rstd * weight does not."""
+    x, w = _rand((70, 544), 61, 0.3, dt).clamp(-1.9, 1.9) * rows, _rand((544,), 62, 1.0, dt) * weight
+    x[0], w[:32] = rows * 1.5, weight
+    assert torch.isfinite(x).all() and torch.isfinite(w).all()
+    o = _norm(x, None, w, eps=eps)
+    _, _, y = _reference(x, None, w, eps=eps)
+    _close(o["y"], y, _step(dt) + 2.0 ** -40)
+    check_mx(o["y8"], o["scale"], y, 2.0 ** -40)
+
+
 def test_norm_nan_stays_in_its_row():
     x, w = _rand((5, 512), 7, 1.0, torch.bfloat16), _rand((512,), 8, 1.0, torch.bfloat16)
     good = _norm(x, None, w)
