@@ -124,8 +124,9 @@ int moe_combine_backward(const void* dy, int dt, const void* y_perm, int y_perm_
  *   writes them for every expert.  The gradient of token t's row in the
  *   gathered form is the sum of its copies' dx_perm rows: moe_combine with
  *   weights 1.  Shape limits of moe_grouped_ffn; H and I_loc at most
- *   65536, H * I_loc and max_rows at most 2^30, and shapes that a launch of
- *   fewer than 2^32 threads does not cover are MOE_ERR_UNSUPPORTED: in float32
+ *   65536, H * I_loc and max_rows at most 2^30 (in bfloat16 H * I_loc below
+ *   2^30), and shapes that a launch of fewer than 2^32 threads does not cover
+ *   are MOE_ERR_UNSUPPORTED: in float32
  *   from 1.7e10 elements of dx_perm, dw13 and dw2 together, in bfloat16 from
  *   2^28 rows or 2.7e11 elements.
  *   An expert whose offsets leave [0, max_rows] or decrease is treated as one
@@ -160,8 +161,8 @@ int moe_grouped_ffn_backward(const void* dy_perm, const void* x_perm, const void
  *   w13[E_loc][2*I_loc][H] with w13_scale[E_loc][2*I_loc][MOE_MX_PITCH(H)];
  *   w2[E_loc][H][I_loc] with w2_scale[E_loc][H][MOE_MX_PITCH(I_loc)];
  *   y_perm[max_rows][H] of dtype y_dt.  Elements must be finite, scale bytes
- *   below 255 and the values they stand for below 2^127.  Limits, offsets and sources as for
- *   moe_grouped_ffn_train (a source of -1 gives a meaningless row, which
+ *   below 255 and the values they stand for below 2^127.  Limits (H * I_loc at
+ *   most 2^30), offsets and sources as for moe_grouped_ffn_train (a source of -1 gives a meaningless row, which
  *   moe_combine does not read).
  */
 size_t moe_grouped_ffn_mxfp8_workspace_size(int max_rows, int E_loc, int H, int I_loc);

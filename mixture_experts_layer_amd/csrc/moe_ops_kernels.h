@@ -41,7 +41,7 @@ struct TrainFfn {
   void* h;                  // [max_rows][I], workspace
 };
 constexpr int OPS_MAX_DIM = 65536;               // H and I of the expert blocks
-constexpr long long OPS_MAX_HI = 1ll << 30;      // H * I: an expert's weights within 4 GiB
+constexpr long long OPS_MAX_HI = 1ll << 30;      // H * I: 32-bit offsets inside an expert
 constexpr int OPS_MAX_ROWS = 1 << 30;            // rows of the expert blocks
 // whether every launch of a shape holds fewer than 2^32 threads
 bool train_fits(int max_rows, int E, int H, int I, int dt);

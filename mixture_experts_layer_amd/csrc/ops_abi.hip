@@ -45,6 +45,8 @@ int check_train(int max_rows, int E_loc, int H, int I_loc, int dt) {
   if (!valid_dt(dt)) return MOE_ERR_INVALID_ARG;
   const int st = check_block(max_rows, E_loc, H, I_loc);
   if (st) return st;
+  // an expert's W13 within the 2^32 - 1 bytes that a buffer descriptor can span
+  if (dt == MOE_BF16 && (long long)H * I_loc >= OPS_MAX_HI) return MOE_ERR_UNSUPPORTED;
   return train_fits(max_rows, E_loc, H, I_loc, dt) ? MOE_OK : MOE_ERR_UNSUPPORTED;
 }
 int check_mx(int max_rows, int E_loc, int H, int I_loc) {

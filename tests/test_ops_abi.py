@@ -320,3 +320,16 @@ def test_the_saved_projections_may_be_of_the_rows_type(calls):
         assert _st(fn, *dict(a, dt=2 | flag).values()) == INVALID
         q = getattr(M, fn + "_workspace_size")
         assert q(16, 4, 256, 128, 1 | flag) == q(16, 4, 256, 128, 1) > 0 == q(16, 4, 256, 128, flag)
+
+
+def test_experts_of_2_32_bytes_are_refused_in_bfloat16_training():
+    """The gate/up product addresses an expert's W13 by 32-bit offsets and a
+    buffer of at most 2^32 - 1 bytes: 4 H I in bfloat16."""
+    for H, I in ((32768, 32768), (65536, 16384), (16384, 65536)):
+        for fn, a in (("moe_grouped_ffn_train", TRAIN), ("moe_grouped_ffn_backward", BACKWARD)):
+            q = getattr(M, fn + "_workspace_size")
+            assert q(16, 1, H, I, 1) == 0 < q(16, 1, H, I - 32, 1)
+            assert q(16, 1, H, I, 0) > 0                # float32 is read by 64-bit addresses
+            for size, want in ((I, UNSUPPORTED), (I - 32, WORKSPACE)):
+                assert _st(fn, *dict(a, E_loc=1, H=H, I_loc=size, ws_bytes=1).values()) == want
+        assert M.moe_grouped_ffn_mxfp8_workspace_size(16, 1, H, I) > 0      # 2^31 bytes
