@@ -58,8 +58,8 @@ extern "C" {
  *   y8_scale, and rstd may each be NULL, but not all of them.  sum and y may be
  *   x or residual themselves (and not each other).  eps >= 0 and finite; with
  *   eps = 0 a row of zeros has no norm and gives NaN.  H a multiple of 32, at
- *   most 16384, and T * min(H / 8, 1024) below 2^32 (more rows:
- *   MOE_ERR_UNSUPPORTED).
+ *   most 16384, and T * min(64 * ceil(H / 512), 1024) below 2^32, the threads of
+ *   a launch with a block per row (more rows: MOE_ERR_UNSUPPORTED).
  */
 int moe_rmsnorm(const void* x, const void* residual, const void* weight, float eps, int T, int H,
                 int dt, void* sum, void* y, void* y8, uint8_t* y8_scale, float* rstd, void* stream);

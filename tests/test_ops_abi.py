@@ -333,3 +333,14 @@ def test_experts_of_2_32_bytes_are_refused_in_bfloat16_training():
             for size, want in ((I, UNSUPPORTED), (I - 32, WORKSPACE)):
                 assert _st(fn, *dict(a, E_loc=1, H=H, I_loc=size, ws_bytes=1).values()) == want
         assert M.moe_grouped_ffn_mxfp8_workspace_size(16, 1, H, I) > 0      # 2^31 bytes
+
+
+def test_the_documented_limit_of_rows_is_the_one_that_holds():
+    limit = re.search(r"T \* (min\(64 \* ceil\(H / 512\), 1024\))\s*(?:\*\s*)?below 2\^32", open(HEADER).read()).group(1)
+    for H in (32, 512, 544, 4096, 8192, 16384):
+        threads = eval(limit, {"min": min, "ceil": lambda v: int(-(-v // 1)), "H": H})
+        most = (2 ** 32 - 1) // threads
+        for T, want in ((most, INVALID), (most + 1, UNSUPPORTED)):
+            if T < 2 ** 31:
+                assert _st("moe_rmsnorm", *dict(NORM, T=T, H=H, x=None).values()) == want
+                assert _st("moe_combine_backward", *dict(COMBINE, T=T, H=H, k=1, dy=None).values()) == want
