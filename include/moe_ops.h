@@ -87,8 +87,9 @@ int moe_rmsnorm_backward(const void* dy, const void* dsum, const void* s, const 
  *     dy_perm[row] = topk_w[t][j] * dy[t]                      (dtype y_perm_dt)
  *     dtopk_w[t][j] = sum_h dy[t][h] * y_perm[row][h]          (float32)
  *   and dtopk_w[t][j] = 0 where dst_row[t][j] < 0.  The gradient of y_shared
- *   is dy itself.  dst_row names every row at most once, as moe_permute writes
- *   it; rows it does not name keep what dy_perm held (so in a padded layout,
+ *   is dy itself.  dst_row names rows of y_perm and dy_perm (what it
+ *   holds is not checked), every row at most once, as moe_permute writes it;
+ *   rows it does not name keep what dy_perm held (so in a padded layout,
  *   whose blank rows moe_grouped_ffn_backward reads as well, clear dy_perm
  *   first).  dy_perm may be y_perm itself, where no row of it is blank.
  *   Limits of moe_combine, and H and T as for moe_rmsnorm.

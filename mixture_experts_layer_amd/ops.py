@@ -5,7 +5,8 @@ Arguments are contiguous torch tensors on one GPU (or None for NULL).  Unlike
 the raw C entry points, which see only addresses, a call here refuses a tensor
 whose type, layout, size or device is not what the entry point will read; it
 runs on that GPU's current stream unless `stream` names another of its
-streams.
+streams.  What lies in the tensors is not looked at: that src_token names rows
+of x or x8, and dst_row rows of y_perm, is the caller's to hold.
 """
 from __future__ import annotations
 
@@ -114,7 +115,8 @@ def moe_combine_backward(dy, dt, y_perm, y_perm_dt, dst_row, topk_w, T, k, H, dy
     _call("moe_combine_backward",
           (("dy", dy, dt, T * H), ("y_perm", y_perm, y_perm_dt, 0),
            ("dst_row", dst_row, "i", T * k), ("topk_w", topk_w, "f", T * k),
-           ("dy_perm", dy_perm, y_perm_dt, 0), ("dtopk_w", dtopk_w, "f", T * k)),
+           ("dy_perm", dy_perm, y_perm_dt, 0 if y_perm is None else y_perm.numel()),
+           ("dtopk_w", dtopk_w, "f", T * k)),
           (dy, dt, y_perm, y_perm_dt, dst_row, topk_w, T, k, H, dy_perm, dtopk_w), stream)
 
 

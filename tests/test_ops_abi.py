@@ -344,3 +344,21 @@ def test_the_documented_limit_of_rows_is_the_one_that_holds():
             if T < 2 ** 31:
                 assert _st("moe_rmsnorm", *dict(NORM, T=T, H=H, x=None).values()) == want
                 assert _st("moe_combine_backward", *dict(COMBINE, T=T, H=H, k=1, dy=None).values()) == want
+
+
+def test_the_combine_gradient_refuses_rows_shorter_than_those_it_reads(calls):
+    """Every row that dst_row names is read in y_perm and written in dy_perm."""
+    f, i = torch.float32, torch.int32
+
+    def call(y_perm, dy_perm):
+        M.moe_combine_backward(_gpu(4, 64), 1, y_perm, 1, _gpu(4, 2, dt=i), _gpu(4, 2, dt=f), 4, 2, 64, dy_perm,
+                               _gpu(4, 2, dt=f))
+    for rows in (8, 11):
+        call(_gpu(8, 64), _gpu(rows, 64))
+    assert len(calls) == 2
+    for y, dy in ((8, 7), (11, 8)):
+        with pytest.raises(ValueError, match="dy_perm holds .* fewer than"):
+            call(_gpu(y, 64), _gpu(dy, 64))
+    both = _gpu(8, 64)
+    call(both, both)
+    assert len(calls) == 3
