@@ -41,8 +41,8 @@ extern "C" {
 /* Scale bytes of an MXFP8 row of K elements. */
 #define MOE_MX_PITCH(K) (((K) + 127) / 128 * 4)
 /* Added to dt = MOE_BF16: the gate and up projections that a training block
- * saves are bfloat16 as well, not float32. */
-#define MOE_GU_BF16 0x100
+ * saves take 16 bits each, not a float32. */
+#define MOE_GU_16 0x100
 
 /*
  * moe_rmsnorm -- the norm between the residual stream and the layer.
@@ -110,14 +110,19 @@ int moe_combine_backward(const void* dy, int dt, const void* y_perm, int y_perm_
  *               SiLU'(g) = s (1 + g (1 - s)), s = 1 / (1 + exp(-g))
  *               dx_perm[r] = W_gate^T dg + W_up^T du
  *               dw13[i] = sum_r [dg | du] a^T,  dw2[i] = sum_r dy_perm[r] h^T
- *   gu is float32, or bfloat16 with dt = MOE_BF16 | MOE_GU_BF16 in both calls
- *   (the Python binding goes by gu's own type).  The backward pass reads g and u
- *   from gu and forms h anew.  h, dg and du are rounded to dt before the
- *   products that read them, as h is in the forward pass.  A float32 gu holds g
- *   and u unrounded, so a gradient passes one rounding between its two products,
- *   as the output does; a bfloat16 gu takes half the memory and adds the
- *   rounding of g and u (against float64, in 2-norm: dx_perm, dw13 and dw2
- *   2.3e-3 with float32; 3.0e-3, 3.0e-3 and 3.5e-3 with bfloat16).
+ *   gu is float32 and holds g and u unrounded; or, with dt = MOE_BF16 |
+ *   MOE_GU_16 in both calls, it has 16 bits per value and half the memory (the
+ *   Python binding goes by gu's type: a bfloat16 tensor is taken as such
+ *   storage).  What the 16-bit form holds is for these two calls alone, and no
+ *   bfloat16 numbers: four consecutive columns, from a multiple of 4 on, share
+ *   an exponent, and each value is off by at most 2^-11 of itself plus 2^-17 of
+ *   the largest of its four.  A value that is not finite makes the other three
+ *   undefined.
+ *   The backward pass reads g and u from gu and forms h anew.  h, dg and du are
+ *   rounded to dt before the products that read them, as h is in the forward
+ *   pass, so a gradient passes one such rounding between its two products, as
+ *   the output does (bfloat16, against float64, in 2-norm: y_perm and the
+ *   gradients 2.35e-3 with a float32 gu, the gradients 2.37e-3 with 16 bits).
  *
  *   dy_perm, dx_perm, y_perm: [max_rows][H]; dw13, dw2: shapes of w13, w2; all
  *   dtype dt.  dx_perm may be NULL, and dw13 and dw2 together may be NULL (not

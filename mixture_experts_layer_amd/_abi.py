@@ -7,7 +7,7 @@ import os
 MOE_OK = 0
 MOE_F32 = 0
 MOE_BF16 = 1
-MOE_GU_BF16 = 0x100      # include/moe_ops.h
+MOE_GU_16 = 0x100        # include/moe_ops.h
 GATE_TOPK_SOFTMAX = 0
 GATE_SOFTMAX_TOPK = 1
 GATE_SOFTMAX_TOPK_RENORM = 2

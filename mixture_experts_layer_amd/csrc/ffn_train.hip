@@ -39,6 +39,7 @@
 
 namespace moe {
 
+typedef _Float16 f16x2_v __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2_v __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4_v __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ bf16x8_t tr_join(u32x2_v lo, u32x2_v hi) {
@@ -66,7 +67,7 @@ struct GemmArgs {
   long long out_stride;       // elements between experts' outputs (weight gradients)
   bf16_t* out2;               // EPI_SWIGLU, EPI_DSWIGLU: h [rows][N]
   void* gu;                   // [rows][2 N] of EPI_SWIGLU (written) and EPI_DSWIGLU (read)
-  bool gu_bf16;               // its type, else float32
+  bool gu16;                  // its form: 16 bits per value, else float32
 };
 
 // Tile shape: TM x TN outputs, STAGES buffers of 64 along the contraction,
@@ -145,10 +146,35 @@ __device__ __forceinline__ void load4(const float* p, float (&f)[4]) {
   const float4 v = *reinterpret_cast<const float4*>(p);
   f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
 }
+
+// The 16-bit form of gu: four consecutive values, scaled by a power of two so
+// that the largest lies in [2^-8, 2^-7), as IEEE halves, whose two upper
+// exponent bits are then zero; in their place stand the 8 bits of the largest
+// value's float32 exponent, two in each half.  In bfloat16, in the same memory,
+// a value would keep 8 significant bits, here 11 (gradients 3.5e-3 from float64
+// there, 2.4e-3 here), and the range is float32's all the same.  A
+// value that is not finite takes the group's largest code and exponent 255,
+// which reads as infinite.
+__device__ __forceinline__ uint2 gu_pack4(float a, float b, float c, float d) {
+  const uint32_t top = max(max(__float_as_uint(a) & 0x7f800000u, __float_as_uint(b) & 0x7f800000u),
+                           max(__float_as_uint(c) & 0x7f800000u, __float_as_uint(d) & 0x7f800000u));
+  const int e = (int)(top >> 23);
+  constexpr float MOST = 0x1.ffcp-8f;      // the largest half below 2^-7
+  auto half = [&](float v) { return fminf(fmaxf(ldexpf(v, 119 - e), -MOST), MOST); };
+  const uint32_t lo =
+      __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_v){half(a), half(b)}, f16x2_v));
+  const uint32_t hi =
+      __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_v){half(c), half(d)}, f16x2_v));
+  return make_uint2(lo | (e & 3) << 13 | (e >> 2 & 3) << 29, hi | (e >> 4 & 3) << 13 | (e >> 6) << 29);
+}
+// (a row of the 16-bit form)
 __device__ __forceinline__ void load4(const bf16_t* p, float (&f)[4]) {
   const uint2 v = *reinterpret_cast<const uint2*>(p);
-  f[0] = __uint_as_float(v.x << 16); f[1] = __uint_as_float(v.x & 0xffff0000u);
-  f[2] = __uint_as_float(v.y << 16); f[3] = __uint_as_float(v.y & 0xffff0000u);
+  const int e = (int)((v.x >> 13 & 3) | (v.x >> 27 & 12) | (v.y >> 9 & 48) | (v.y >> 23 & 192));
+  const f32x2_v lo = __builtin_convertvector(__builtin_bit_cast(f16x2_v, v.x & 0x9fff9fffu), f32x2_v);
+  const f32x2_v hi = __builtin_convertvector(__builtin_bit_cast(f16x2_v, v.y & 0x9fff9fffu), f32x2_v);
+  f[0] = ldexpf(lo[0], e - 119); f[1] = ldexpf(lo[1], e - 119);
+  f[2] = ldexpf(hi[0], e - 119); f[3] = ldexpf(hi[1], e - 119);
 }
 
 // One output tile: rows [r0, r1) (of expert e; in a weight gradient, rows of the
@@ -469,19 +495,20 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, unsigned char* smem
     store(out, a.ldo);
   }
   if constexpr (EPI == EPI_SWIGLU) {
-    // g, u (TN / 2 columns of float32 fill a staged row of TN bfloat16; in
-    // bfloat16 both fit side by side), then h
+    // g, u (TN / 2 columns of float32 fill a staged row of TN bfloat16; of 16
+    // bits both fit side by side), then h
     constexpr int HALF = C::MFN / 2;
-    if (a.gu_bf16) {
+    if (a.gu16) {
 #pragma unroll
       for (int mi = 0; mi < C::MFM; ++mi)
 #pragma unroll
         for (int ni = 0; ni < C::MFN; ++ni)
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            put(mi, nbase[ni] + 8 * q + 4 * khalf,
-                cvt_bf16x2(acc[mi][ni][4 * q], acc[mi][ni][4 * q + 1]),
-                cvt_bf16x2(acc[mi][ni][4 * q + 2], acc[mi][ni][4 * q + 3]));
+          for (int q = 0; q < 4; ++q) {
+            const f32x16_t& v = acc[mi][ni];
+            const uint2 p = gu_pack4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            put(mi, nbase[ni] + 8 * q + 4 * khalf, p.x, p.y);
+          }
       lds_barrier();
       constexpr int CPR = COLS / 8;
       for (int c = threadIdx.x; c < C::TM * 2 * CPR; c += C::NTHR) {
@@ -592,7 +619,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, unsigned char* smem
         lds_barrier();
       }
     };
-    if (a.gu_bf16) rows(static_cast<const bf16_t*>(a.gu));
+    if (a.gu16) rows(static_cast<const bf16_t*>(a.gu));
     else rows(static_cast<const float*>(a.gu));
   }
 }
@@ -956,7 +983,7 @@ struct Product {
 static GemmArgs bf16_args(const TrainFfn& f, const Product& p) {
   return GemmArgs{(const bf16_t*)p.A, (const bf16_t*)p.B, p.lda, p.ldb, p.b_stride, p.src,
                   f.offsets, f.E, f.max_rows, p.M, p.N, p.K, p.up_off, (bf16_t*)p.out, p.ldo,
-                  p.out_stride, (bf16_t*)p.out2, f.gu, f.gu_bf16};
+                  p.out_stride, (bf16_t*)p.out2, f.gu, f.gu16};
 }
 static F32GemmArgs f32_args(const TrainFfn& f, const Product& p) {
   return F32GemmArgs{(const float*)p.A, (const float*)p.B, p.lda, p.ldb, p.b_stride, p.src,

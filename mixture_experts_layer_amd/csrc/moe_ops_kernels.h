@@ -37,7 +37,7 @@ struct TrainFfn {
   const void* w13;
   const void* w2;
   void* gu;                 // [max_rows][2 I]: written by the forward pass, read by the backward
-  bool gu_bf16;             // its type (bfloat16 rows; else float32)
+  bool gu16;                // its form: 16 bits per value (bfloat16 rows only), else float32
   void* h;                  // [max_rows][I], workspace
 };
 constexpr int OPS_MAX_DIM = 65536;               // H and I of the expert blocks

@@ -39,8 +39,8 @@ int check_block(int max_rows, int E_loc, int H, int I_loc) {
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
-// The rows' type of a training block's dt, which may say that gu is bfloat16.
-int rows_dt(int dt) { return dt == (MOE_BF16 | MOE_GU_BF16) ? MOE_BF16 : dt; }
+// The rows' type of a training block's dt, which may say that gu has 16 bits per value.
+int rows_dt(int dt) { return dt == (MOE_BF16 | MOE_GU_16) ? MOE_BF16 : dt; }
 int check_train(int max_rows, int E_loc, int H, int I_loc, int dt) {
   if (!valid_dt(dt)) return MOE_ERR_INVALID_ARG;
   const int st = check_block(max_rows, E_loc, H, I_loc);
@@ -118,7 +118,7 @@ int moe_grouped_ffn_train(const void* x_perm, const void* x, const int32_t* src_
                           const int32_t* offsets, int E_loc, int max_rows, int H, int I_loc,
                           const void* w13, const void* w2, int dt, void* gu, void* y_perm,
                           void* ws, size_t ws_bytes, void* stream) {
-  const bool gu_bf16 = dt != rows_dt(dt);
+  const bool gu16 = dt != rows_dt(dt);
   dt = rows_dt(dt);
   const int st = check_train(max_rows, E_loc, H, I_loc, dt);
   if (st) return st;
@@ -130,7 +130,7 @@ int moe_grouped_ffn_train(const void* x_perm, const void* x, const int32_t* src_
   if (!ws || ws_bytes < moe_grouped_ffn_train_workspace_size(max_rows, E_loc, H, I_loc, dt))
     return MOE_ERR_WORKSPACE;
   const TrainFfn f{x_perm ? x_perm : x, x_perm ? nullptr : src_token, offsets, E_loc, max_rows, H,
-                   I_loc, dt, w13, w2, gu, gu_bf16, ws};
+                   I_loc, dt, w13, w2, gu, gu16, ws};
   return hip_status(launch_train_forward(f, y_perm, static_cast<hipStream_t>(stream)));
 }
 
@@ -146,7 +146,7 @@ int moe_grouped_ffn_backward(const void* dy_perm, const void* x_perm, const void
                              int max_rows, int H, int I_loc, const void* w13, const void* w2,
                              int dt, const void* gu, void* dx_perm, void* dw13, void* dw2,
                              void* ws, size_t ws_bytes, void* stream) {
-  const bool gu_bf16 = dt != rows_dt(dt);
+  const bool gu16 = dt != rows_dt(dt);
   dt = rows_dt(dt);
   const int st = check_train(max_rows, E_loc, H, I_loc, dt);
   if (st) return st;
@@ -170,7 +170,7 @@ int moe_grouped_ffn_backward(const void* dy_perm, const void* x_perm, const void
   void* dgu = c.take<char>((size_t)max_rows * I_loc * elt_bytes(dt) * 2);
   void* xp = c.take<char>((size_t)max_rows * H * elt_bytes(dt));
   const TrainFfn f{x_perm ? x_perm : x, x_perm ? nullptr : src_token, offsets, E_loc, max_rows, H,
-                   I_loc, dt, w13, w2, const_cast<void*>(gu), gu_bf16, h};
+                   I_loc, dt, w13, w2, const_cast<void*>(gu), gu16, h};
   return hip_status(launch_train_backward(f, dy_perm, dgu, xp, dx_perm, dw13, dw2, s));
 }
 

@@ -10,7 +10,7 @@ of x or x8, and dst_row rows of y_perm, is the caller's to hold.
 """
 from __future__ import annotations
 
-from ._abi import MOE_BF16, MOE_F32, MOE_GU_BF16
+from ._abi import MOE_BF16, MOE_F32, MOE_GU_16
 
 
 def mx_pitch(K: int) -> int:
@@ -77,12 +77,12 @@ def _launch(fn, argv, dev, stream):
 
 def _gu(gu, dt):
     """dt of a training block's rows, its gu's type for _call, and dt as the
-    library takes it: bfloat16 rows may save gu in either type."""
-    dt &= ~MOE_GU_BF16
+    library takes it: with bfloat16 rows a gu of that type is the 16-bit form."""
+    dt &= ~MOE_GU_16
     if _LIB is None:
         _setup()
     if dt == MOE_BF16 and gu is not None and gu.dtype == _TYPES[MOE_BF16][0]:
-        return dt, MOE_BF16, dt | MOE_GU_BF16
+        return dt, MOE_BF16, dt | MOE_GU_16
     return dt, "f", dt
 
 

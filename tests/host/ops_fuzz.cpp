@@ -54,7 +54,7 @@ const int kRows[] = {INT_MIN, -1, 0, 1, 2, 15, 16, 63, 64, 65, 255, 256, 257, 81
 const int kWidth[] = {INT_MIN, -32, 0, 1, 31, 32, 48, 64, 96, 512, 544, 4096, 8192, 14336, 16384, 16416, 32768, 65504,
                       65536, 65568, INT_MAX - 31, INT_MAX};
 const int kExperts[] = {INT_MIN, -1, 0, 1, 2, 8, 60, 128, 1000, 1024, 1025, INT_MAX};
-const int kDt[] = {INT_MIN, -1, 0, 1, 2, MOE_GU_BF16, MOE_BF16 | MOE_GU_BF16, 2 | MOE_GU_BF16, INT_MAX};
+const int kDt[] = {INT_MIN, -1, 0, 1, 2, MOE_GU_16, MOE_BF16 | MOE_GU_16, 2 | MOE_GU_16, INT_MAX};
 
 wide cdiv(wide a, wide b) { return (a + b - 1) / b; }
 
@@ -67,7 +67,7 @@ bool block_ok(int rows, int E, int H, int I) {
   return rows >= 0 && rows <= (1 << 30) && E >= 1 && E <= 1024 && H > 0 && H % 32 == 0 && H <= 65536 && I > 0 &&
          I % 32 == 0 && I <= 65536 && (wide)H * I <= ((wide)1 << 30);
 }
-bool train_dt(int dt) { return dt == 0 || dt == 1 || dt == (MOE_BF16 | MOE_GU_BF16); }
+bool train_dt(int dt) { return dt == 0 || dt == 1 || dt == (MOE_BF16 | MOE_GU_16); }
 
 }  // namespace
 
@@ -123,7 +123,7 @@ int main(int argc, char** argv) {
     const bool blk = block_ok(T, E, H, I);
     const int rows = T;
     {
-      const int rdt = dt & ~MOE_GU_BF16;
+      const int rdt = dt & ~MOE_GU_16;
       const size_t f = moe_grouped_ffn_train_workspace_size(rows, E, H, I, dt);
       const size_t b = moe_grouped_ffn_backward_workspace_size(rows, E, H, I, dt);
       CHECK((f > 0) == (b > 0), "train sizes of rows %d E %d H %d I %d dt %d", rows, E, H, I, dt);

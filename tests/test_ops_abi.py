@@ -291,8 +291,9 @@ def _gpu(*shape, dt=torch.bfloat16):
 
 
 def test_the_saved_projections_may_be_of_the_rows_type(calls):
-    """gu of a bfloat16 block is float32 or bfloat16, as the caller has it; the
-    C entries read which from dt, and the binding from the tensor."""
+    """gu of a bfloat16 block is float32 or a bfloat16 tensor for the 16-bit form,
+    as the caller has it; the C entries read which from dt, and the binding from
+    the tensor."""
     b, f, i = torch.bfloat16, torch.float32, torch.int32
     z = _gpu
 
@@ -304,7 +305,7 @@ def test_the_saved_projections_may_be_of_the_rows_type(calls):
         M.moe_grouped_ffn_backward(z(4, 64, dt=t), None, z(4, 64, dt=t), z(4, dt=i), z(3, dt=i), 2, 4, 64, 32,
                                    z(2, 64, 64, dt=t), z(2, 64, 32, dt=t), dt, gu, z(4, 64, dt=t), None, None,
                                    z(64, dt=torch.uint8), 64)
-    flag = int(re.search(r"#define MOE_GU_BF16 (\w+)", open(HEADER).read()).group(1), 0)
+    flag = int(re.search(r"#define MOE_GU_16 (\w+)", open(HEADER).read()).group(1), 0)
     for call, at in ((train, 10), (backward, 11)):
         for t, gu, dt, want in ((b, z(4, 64), 1, 1 | flag), (b, z(4, 64, dt=f), 1, 1), (f, z(4, 64, dt=f), 0, 0)):
             call(t, gu, dt)
