@@ -23,7 +23,9 @@
 //
 // Measured on MI355X, Qwen3 shape (128 experts, H 4096, I 1536): T = 64 462 us,
 // 5.3 TB/s of weights (a large copy: 5.1); T = 8192 gate/up 1.10 ms and down 0.61,
-// 1.4-1.5 PFLOP/s, bound by operand loads beyond L2 (matrix cores busy 0.36-0.39).
+// 1.4-1.5 PFLOP/s.  There neither memory (2.6 TB/s) nor the matrix cores (busy
+// 0.36-0.39) are full: 256-row tiles have one block per CU and two stages, so
+// every chunk of 128 waits for the last of its own loads.
 // One token of an eighth of it (I 192): 11 us in two launches, latency.
 #include <algorithm>
 #include <type_traits>

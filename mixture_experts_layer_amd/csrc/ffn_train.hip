@@ -25,11 +25,12 @@
 //
 // Both reach LDS by 16-byte direct loads (1 KB per wave instruction).
 //
-// Measured on MI355X.  Mixtral shape, 8 experts, T = 4096 (R = 8192 rows): gate/up
-// 1.98 ms, down 0.95, dh 1.20, dx 1.84, both weight gradients 3.04: 0.80 to 1.05
-// PFLOP/s, matrix cores busy 0.50-0.54 at 1.85-1.95 GHz (dh 0.40: its epilogue
-// moves 1.6 GB).  Qwen3 shape, 128 experts, 32 rows each: bound by the weights and
-// their gradients, 14.5 GB in 2.65 ms.
+// Measured on MI355X.  Mixtral shape, 8 experts, T = 4096 (R = 8192 rows), gu of 16
+// bits: gate/up 1.98 ms, down 0.95, dh 1.14, dx 1.83, both weight gradients 3.07:
+// 0.84 to 1.05 PFLOP/s, matrix cores busy 0.49-0.55 at 1.84-1.91 GHz (dh 0.43: its
+// epilogue moves 1.2 GB; with a float32 gu 1.6 GB, dh 1.21 ms and gate/up 2.00).
+// Qwen3 shape, 128 experts, 32 rows each: bound by the weights and their
+// gradients, 14.5 GB in 2.63 ms.
 #include <algorithm>
 #include <type_traits>
 
@@ -713,8 +714,11 @@ __global__ __launch_bounds__(256) void train_gather_kernel(const uint4* x, const
 // gradient alone, where a few rows per expert leave nothing to split.)  A lane's
 // four elements of a chunk feed four products: element i of lane l stands for
 // k = 4 (l / 16) + i in both operands.  The toy layer's step takes 34 us, four
-// dependent launches bound by their chains of loads (64 x 64 tiles of plain
-// multiply-adds: 343 us); three to six chunks in flight took 36 to 45.
+// dependent launches bound by each wave's chain of loads, 4 to 16 chunks long (dx
+// contracts over 2 I: 15 us; 64 x 64 tiles of plain multiply-adds: 343 us the
+// step); three to six chunks in flight took 36 to 45.  Larger layers reach a
+// quarter of the float32 product rate (8 experts of 128 rows, H 1024, I 512: 252
+// us, 38 TFLOP/s): a 32 x 32 tile loads an operand byte for every 8 operations.
 // ---------------------------------------------------------------------------
 struct F32GemmArgs {
   const float* A;

@@ -8,8 +8,8 @@
 // row in registers, 8 consecutive elements (16 bytes of bfloat16) per thread
 // and step, so every input is read once and the row never goes back to memory
 // between its statistics and its outputs.  Measured on MI355X (a large copy:
-// 5.09 TB/s): 8192 x 4096 bfloat16 with a residual to sum, y and MXFP8 55 us,
-// 5.4 TB/s; backward of 8191 x 7168 with dsum 96 us, 4.9 TB/s; one row of 4096
+// 5.09 TB/s): 8192 x 4096 bfloat16 with a residual to sum, y and MXFP8 52 to 55
+// us, 5.5 TB/s; backward of 8191 x 7168 with dsum 96 us, 4.9 TB/s; one row of 4096
 // 2.8 us, a launch and one chain of loads.
 #include "moe_ops_device.h"
 #include "moe_ops_kernels.h"
@@ -251,7 +251,9 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float* part, int
 //   dy_perm[dst_row[t][j]] = w[t][j] * dy[t],   dw[t][j] = <dy[t], y_perm[row]>.
 // Rows belong to one (token, slot) each, so a block per token writes its own
 // rows and no two blocks meet.  dy[t] stays in registers over the slots.
-// Memory-bound: T = 8192, k = 8, H = 4096 in bfloat16 takes 228 us, 5.0 TB/s.
+// Memory-bound: T = 8192, k = 8, H = 4096 in bfloat16 takes 228 us, 5.0 TB/s.  With
+// fewer tokens than CUs each busy CU moves all slots of its token, and the others
+// nothing: T = 33, k = 8, H = 7168 7 us, 0.24 MB per block.
 // ---------------------------------------------------------------------------
 struct CombineBwdArgs {
   const void* dy;
